@@ -284,6 +284,119 @@ int msgla_launch_plan(const msgla_handle* h, int B, int L, char* names, size_t l
  * pages (it exercises this library's own bounded waits). */
 int msgla_test_skip_arrival(msgla_handle* h, int enable);
 
+/* ---- operators next to the layer. They need no handle: every call names its device
+ * and element type in a small configuration, reads and writes the caller's buffers
+ * only, keeps nothing between calls and is asynchronous on `stream` (NULL = legacy
+ * default stream), so calls may overlap on different streams and threads and may be
+ * captured into a CUDA graph. The calling thread's current device is left as it was.
+ * Sums, states and statistics are held in f32. Nothing is reduced by atomics: the
+ * same inputs give the same bits. */
+typedef enum msgla_dtype { MSGLA_BF16 = 0, MSGLA_F16 = 1, MSGLA_F32 = 2 } msgla_dtype;
+
+/* Rows of channels: element (b, l, c) at data[b * batch_stride + l * row_stride + c],
+ * strides in elements, >= 0 and below 2^46; `data` is aligned to its element. Inputs may
+ * be views (halves of a fused projection, expanded rows with stride 0, [L, B, C]
+ * memory read as [B, L, C]). An output's elements have to be distinct, and the span
+ * of an output, from its first to its last element, must not meet the span of an
+ * input or of another output. */
+typedef struct msgla_rows {
+  void* data;
+  long long batch_stride, row_stride;
+} msgla_rows;
+
+/* Gated recurrence, the GLA recurrence of Sec. 2.1 with one state per channel (an
+ * element-wise gate and no key: the notes' S_t with Diag(alpha_t) alone), for a batch
+ * of B sequences of L rows of D channels, with gate logits z in the layer's form:
+ *     log a_t = logsigmoid(z_t) / gate_normalizer
+ *     h_t = a_t h_{t-1} + u_t,   u_t = x_t,  or (1 - a_t) x_t when tied = 1. */
+typedef struct msgla_scan_config {
+  int device;             /* CUDA device of every buffer                               */
+  int dtype;              /* msgla_dtype of x, z, h and of their gradients              */
+  int D;                  /* channels, 1..2^24                                          */
+  int tied;               /* 0: u = x, 1: u = (1 - a) x                                  */
+  float gate_normalizer;  /* > 0, finite                                                 */
+} msgla_scan_config;
+
+/* Bytes of the states that a forward keeps for its backward: f32
+ * [B, ceil(L / 64), D], the state before rows 0, 64, 128, ... of every sequence. */
+int msgla_scan_saved_size(const msgla_scan_config* cfg, int B, int L, size_t* bytes);
+
+/* h = recurrence(x, z), B in [0, 65535], L >= 0.
+ *   x, z     [B, L, D]; z = -inf empties the state before its row (a = 0).
+ *   M        device uint8 [B, L], nonzero = valid, or NULL. A padded row leaves the
+ *            state as it is, its output is zero, and nothing of its x and z is read.
+ *   h0       f32 [B, D], the state before the first row, or NULL (zeros).
+ *   h        [B, L, D].
+ *   h_last   f32 [B, D], the state after the last row (L = 0: h0). May be h0 itself.
+ *   saved    msgla_scan_saved_size bytes, 4-byte aligned, for msgla_scan_backward; or NULL. */
+int msgla_scan_forward(const msgla_scan_config* cfg, int B, int L, const msgla_rows* x, const msgla_rows* z,
+                       const void* M, const float* h0, const msgla_rows* h, float* h_last, float* saved,
+                       void* stream);
+
+/* Gradients of msgla_scan_forward for the same cfg, x, z, M and its `saved`.
+ *   dh        [B, L, D], or NULL (zeros). Not read at padded rows.
+ *   dh_last   f32 [B, D], the gradient of h_last, or NULL (zeros).
+ *   dx, dz    [B, L, D]; zero at padded rows.
+ *   dh0       f32 [B, D], or NULL when not wanted. May be dh_last itself. */
+int msgla_scan_backward(const msgla_scan_config* cfg, int B, int L, const msgla_rows* x, const msgla_rows* z,
+                        const void* M, const float* saved, const msgla_rows* dh, const float* dh_last,
+                        const msgla_rows* dx, const msgla_rows* dz, float* dh0, void* stream);
+
+/* One token of each of B sequences (B in [0, 65535]): the recurrence's row for the
+ * state in `state` (f32 [B, D], read and updated), which then stands after the token.
+ *   x, z, h  rows [B, D] (batch_stride alone is used).
+ *   M        device uint8 [B] or NULL: where it is 0 the state stays, h is zero and
+ *            nothing of x and z is read. */
+int msgla_scan_step(const msgla_scan_config* cfg, int B, const msgla_rows* x, const msgla_rows* z, const void* M,
+                    float* state, const msgla_rows* h, void* stream);
+
+typedef enum msgla_activation { MSGLA_ACT_NONE = 0, MSGLA_ACT_SILU = 1, MSGLA_ACT_SIGMOID = 2 } msgla_activation;
+
+/* Group normalisation, channels last, with an activation or an output gate (the
+ * per-head normalisation of Sec. 3.2 in its general form): for N samples of S rows of
+ * C channels in `groups` groups of neighbouring channels, over the valid rows of one
+ * sample and the channels of one group,
+ *     xhat = (x - mean) / sqrt(var + eps),   or  x / sqrt(mean(x^2) + eps) when center = 0
+ *     v = xhat * weight + bias,   y = act(v),  or  v * act(gate) with a gate.
+ * S = 1 normalises every row by itself (the heads of a token). */
+typedef struct msgla_norm_config {
+  int device;      /* CUDA device of every buffer                                      */
+  int dtype;       /* msgla_dtype of x, gate, y and of their gradients                  */
+  int C, groups;   /* channels 1..2^24; groups >= 1 divides C                           */
+  int activation;  /* msgla_activation                                                  */
+  int center;      /* 1: mean and variance, 0: root mean square                          */
+  float eps;       /* > 0, finite                                                        */
+} msgla_norm_config;
+
+/* Bytes of device workspace of a forward (gradients = 0) or a backward (1). N and S
+ * are >= 0, N * groups and N * S below 2^31. */
+int msgla_group_norm_workspace_size(const msgla_norm_config* cfg, long long N, long long S, int gradients,
+                                    size_t* bytes);
+
+/*   x, gate  [N, S, C]; gate may be NULL.
+ *   weight, bias  f32 [C], or NULL (ones, zeros).
+ *   M        device uint8 [N, S], nonzero = valid, or NULL. Padded rows enter no
+ *            statistic, their output is zero and they are not read.
+ *   y        [N, S, C].
+ *   stats    f32 [N, groups, 2], mean (0 when center = 0) and 1 / sqrt(var + eps), for
+ *            the backward; or NULL.
+ *   workspace  msgla_group_norm_workspace_size bytes, 256-byte aligned; calls that may
+ *            overlap need one each. NULL when that size is 0. */
+int msgla_group_norm_forward(const msgla_norm_config* cfg, long long N, long long S, const msgla_rows* x,
+                             const msgla_rows* gate, const float* weight, const float* bias, const void* M,
+                             const msgla_rows* y, float* stats, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+/* Gradients for the same cfg, x, gate, weight, bias and M, and the forward's `stats`.
+ *   dy, dx, dgate  [N, S, C] (dgate NULL exactly when gate is). Padded rows of dy are
+ *            not read, those of dx and dgate are zero.
+ *   dweight, dbias  f32 [C], each may be NULL when not wanted. */
+int msgla_group_norm_backward(const msgla_norm_config* cfg, long long N, long long S, const msgla_rows* x,
+                              const msgla_rows* gate, const float* weight, const float* bias, const void* M,
+                              const float* stats, const msgla_rows* dy, const msgla_rows* dx,
+                              const msgla_rows* dgate, float* dweight, float* dbias, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
 /* Static description of an error code. */
 const char* msgla_status_string(int status);
 

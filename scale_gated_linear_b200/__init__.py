@@ -8,6 +8,12 @@ PyTorch provides device memory and streams.
     layer = MSGLA(d=1024, scales=(1, 2, 4), heads=(2, 1, 1), d_k=256, d_v=512,
                   weights=weights_dict, device=0)
     O = layer(X)          # X: cuda bf16 [B, L, d] -> O: cuda bf16 [B, L, d]
+
+Operators next to the layer, with gradients (see the module ops):
+
+    from scale_gated_linear_b200 import gated_scan, gated_scan_step, group_norm
+    h, last = gated_scan(x, gate)                      # h_t = a_t h_{t-1} + x_t per channel
+    y = group_norm(h.flatten(0, 1), 4, w, b, gate=g, activation="silu")
 """
 from __future__ import annotations
 
@@ -18,7 +24,11 @@ from . import _lib
 from ._lib import (MSGLAError, WS_FUSION, WS_GAMMA, WS_KS, WS_MID, WS_O, WS_POOLED, WS_QS, WS_U, WS_V,
                    WS_Y)
 
-__all__ = ["MSGLA", "MSGLAError", "load_library"]
+from .ops import (gated_scan, gated_scan_backward, gated_scan_forward, gated_scan_step, group_norm,
+                  group_norm_backward, group_norm_forward)
+
+__all__ = ["MSGLA", "MSGLAError", "load_library", "gated_scan", "gated_scan_forward", "gated_scan_backward",
+           "gated_scan_step", "group_norm", "group_norm_forward", "group_norm_backward"]
 
 
 def load_library():

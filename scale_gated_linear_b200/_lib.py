@@ -39,6 +39,19 @@ class Weights(ctypes.Structure):
                 ("norm_w", c_void_p * MAX_SCALES)]
 
 
+class Rows(ctypes.Structure):
+    _fields_ = [("data", c_void_p), ("batch_stride", c_longlong), ("row_stride", c_longlong)]
+
+
+class ScanConfig(ctypes.Structure):
+    _fields_ = [("device", c_int), ("dtype", c_int), ("D", c_int), ("tied", c_int), ("gate_normalizer", c_float)]
+
+
+class NormConfig(ctypes.Structure):
+    _fields_ = [("device", c_int), ("dtype", c_int), ("C", c_int), ("groups", c_int), ("activation", c_int),
+                ("center", c_int), ("eps", c_float)]
+
+
 class MSGLAError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"{STATUS.get(status, status)}: {message}")
@@ -66,6 +79,22 @@ _SIGNATURES = {
     "msgla_step_workspace_size": (c_int, [c_void_p, c_int, POINTER(c_size_t)]),
     "msgla_step": (c_int, [c_void_p, c_void_p, c_void_p, c_int, c_longlong, c_void_p, c_void_p, c_size_t,
                            c_void_p]),
+    "msgla_scan_saved_size": (c_int, [POINTER(ScanConfig), c_int, c_int, POINTER(c_size_t)]),
+    "msgla_scan_forward": (c_int, [POINTER(ScanConfig), c_int, c_int, POINTER(Rows), POINTER(Rows), c_void_p, c_void_p,
+                                   POINTER(Rows), c_void_p, c_void_p, c_void_p]),
+    "msgla_scan_backward": (c_int, [POINTER(ScanConfig), c_int, c_int, POINTER(Rows), POINTER(Rows), c_void_p,
+                                    c_void_p, POINTER(Rows), c_void_p, POINTER(Rows), POINTER(Rows), c_void_p,
+                                    c_void_p]),
+    "msgla_scan_step": (c_int, [POINTER(ScanConfig), c_int, POINTER(Rows), POINTER(Rows), c_void_p, c_void_p,
+                                POINTER(Rows), c_void_p]),
+    "msgla_group_norm_workspace_size": (c_int, [POINTER(NormConfig), c_longlong, c_longlong, c_int,
+                                                POINTER(c_size_t)]),
+    "msgla_group_norm_forward": (c_int, [POINTER(NormConfig), c_longlong, c_longlong, POINTER(Rows), POINTER(Rows),
+                                         c_void_p, c_void_p, c_void_p, POINTER(Rows), c_void_p, c_void_p, c_size_t,
+                                         c_void_p]),
+    "msgla_group_norm_backward": (c_int, [POINTER(NormConfig), c_longlong, c_longlong, POINTER(Rows), POINTER(Rows),
+                                          c_void_p, c_void_p, c_void_p, c_void_p, POINTER(Rows), POINTER(Rows),
+                                          POINTER(Rows), c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
     "msgla_status_string": (c_char_p, [c_int]),
     "msgla_last_error": (c_char_p, []),
 }

@@ -13,8 +13,9 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libmsgla.so")
-SOURCES = ["msgla_abi.cu", "k_gemm.cu", "k_gla.cu", "k_aux.cu", "k_pool.cu", "k_decode.cu"]
-HEADERS = ["msgla_internal.h", "sm100_ptx.cuh"]
+SOURCES = ["msgla_abi.cu", "k_gemm.cu", "k_gla.cu", "k_aux.cu", "k_pool.cu", "k_decode.cu", "k_scan.cu", "k_norm.cu",
+           "ops_abi.cu"]
+HEADERS = ["msgla_internal.h", "ops_internal.h", "sm100_ptx.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

@@ -22,6 +22,7 @@
 
 #include "../../include/msgla.h"
 #include "msgla_internal.h"
+#include "ops_internal.h"
 #include "sm100_ptx.cuh"
 
 using namespace msgla;
@@ -146,6 +147,15 @@ struct DeviceGuard {
 };
 
 }  // namespace
+
+int msgla::set_error(int code, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  return fail(code, "%s", buf);
+}
 
 // ---------------------------------------------------------------- handle
 struct Branch {

@@ -1,0 +1,82 @@
+// ops_internal.h -- parameter blocks and device helpers shared by the gated
+// recurrence (k_scan.cu), group normalisation (k_norm.cu) and their C entry
+// points (ops_abi.cu). Not part of the public interface.
+#pragma once
+#include <cstddef>
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+namespace msgla {
+
+// Records `fmt` as the calling thread's last error and returns `code`.
+int set_error(int code, const char* fmt, ...);
+
+// Rows of channels: element (b, l, c) at ptr[b * batch + l * row + c].
+struct Rows {
+  void* ptr;
+  long long batch, row;
+};
+
+// ---------------------------------------------------------------- gated recurrence
+constexpr int kScanSave = 64;  // rows between two saved states
+
+struct ScanParams {
+  int dtype, B, L, D, tied;
+  float inv_tau;
+  Rows x, z, h, dh, dx, dz;
+  const uint8_t* mask;  // [B, L] or null
+  const float* h0;      // [B, D] or null (zeros)
+  float* last;          // [B, D]
+  float* saved;         // [B, ceil(L / kScanSave), D] states before rows 0, kScanSave, ...; or null
+  const float* dlast;   // [B, D] or null
+  float* dh0;           // [B, D] or null
+};
+cudaError_t launch_scan_forward(const ScanParams& p, cudaStream_t st);
+cudaError_t launch_scan_backward(const ScanParams& p, cudaStream_t st);
+
+struct StepParams {
+  int dtype, B, D, tied;
+  float inv_tau;
+  const void *x, *z;
+  void* h;
+  long long x_row, z_row, h_row;
+  const uint8_t* mask;  // [B] or null
+  float* state;         // [B, D]
+};
+cudaError_t launch_scan_step(const StepParams& p, cudaStream_t st);
+
+// ---------------------------------------------------------------- group normalisation
+struct NormParams {
+  int dtype, C, G, act, center;
+  float eps;
+  long long N, S;
+  Rows x, gate, y, dy, dx, dgate;  // gate.ptr null: no gate
+  const float *w, *b;              // [C] or null (ones, zeros)
+  const uint8_t* mask;             // [N, S] or null
+  float* stats;                    // [N, G, 2] mean and 1 / sqrt(var + eps); forward: may be null
+  float *dw, *db;                  // [C] or null
+  void* workspace;
+};
+size_t norm_workspace(const NormParams& p, bool backward);
+cudaError_t launch_norm_forward(const NormParams& p, cudaStream_t st);
+cudaError_t launch_norm_backward(const NormParams& p, cudaStream_t st);
+
+// ---------------------------------------------------------------- element types
+enum : int { kBF16 = 0, kF16 = 1, kF32 = 2 };
+enum : int { kActNone = 0, kActSilu = 1, kActSigmoid = 2 };
+
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+__device__ __forceinline__ float to_f32(float v) { return v; }
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) { return v; }
+
+}  // namespace msgla
