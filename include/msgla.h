@@ -321,7 +321,7 @@ typedef struct msgla_scan_config {
  * [B, ceil(L / 64), D], the state before rows 0, 64, 128, ... of every sequence. */
 int msgla_scan_saved_size(const msgla_scan_config* cfg, int B, int L, size_t* bytes);
 
-/* h = recurrence(x, z), B in [0, 65535], L >= 0.
+/* h = recurrence(x, z), B in [0, 65535], L in [0, 2^30].
  *   x, z     [B, L, D]; z = -inf empties the state before its row (a = 0).
  *   M        device uint8 [B, L], nonzero = valid, or NULL. A padded row leaves the
  *            state as it is, its output is zero, and nothing of its x and z is read.

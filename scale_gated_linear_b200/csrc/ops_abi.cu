@@ -95,7 +95,7 @@ int check_scan(const msgla_scan_config* c, int B, int L) {
   if (!(c->gate_normalizer > 0.f) || !std::isfinite(c->gate_normalizer) || !std::isfinite(1.f / c->gate_normalizer))
     return set_error(MSGLA_ERR_INVALID_ARG, "gate_normalizer must be positive and finite, and so its reciprocal");
   if (B < 0 || B > 65535) return set_error(MSGLA_ERR_INVALID_ARG, "B=%d outside [0, 65535]", B);
-  if (L < 0) return set_error(MSGLA_ERR_INVALID_ARG, "L=%d must be >= 0", L);
+  if (L < 0 || L > 1 << 30) return set_error(MSGLA_ERR_INVALID_ARG, "L=%d outside [0, 2^30]", L);
   return MSGLA_OK;
 }
 

@@ -24,6 +24,7 @@ constexpr int kScanSave = 64;  // rows between two saved states
 
 struct ScanParams {
   int dtype, B, L, D, tied;
+  int cluster;          // blocks per channel tile (set by the launches)
   float inv_tau;
   Rows x, z, h, dh, dx, dz;
   const uint8_t* mask;  // [B, L] or null

@@ -47,7 +47,7 @@ def test_scan_sizes():
         assert lib.msgla_scan_saved_size(scan_cfg(), 3, L, ctypes.byref(n)) == 0 and n.value == 3 * want * 8 * 4
     assert lib.msgla_scan_saved_size(scan_cfg(D=1 << 20), 65535, 1 << 30, ctypes.byref(n)) == 0
     assert n.value == 65535 * (1 << 24) * (1 << 20) * 4 % 2 ** 64
-    for B, L in ((-1, 1), (65536, 1), (1, -1)):
+    for B, L in ((-1, 1), (65536, 1), (1, -1), (1, (1 << 30) + 1)):
         assert lib.msgla_scan_saved_size(scan_cfg(), B, L, ctypes.byref(n)) == -1
     assert lib.msgla_scan_saved_size(scan_cfg(), 1, 1, None) == -1
     assert lib.msgla_scan_saved_size(None, 1, 1, ctypes.byref(n)) == -1
