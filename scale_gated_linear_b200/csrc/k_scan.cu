@@ -26,6 +26,8 @@
 // and passes the joined pairs through distributed shared memory, one cluster barrier a
 // step. The next step's rows are loaded before this step's are joined.
 #include <cmath>
+#include <cstdlib>
+#include <cstring>
 #include <type_traits>
 
 #include "ops_internal.h"
@@ -35,7 +37,6 @@ namespace msgla {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kTile = 64;  // channels per block
 constexpr int kMaxCluster = 8;
 
 __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
@@ -108,18 +109,18 @@ struct Pair<float> {
   }
 };
 
-// Loads and stores of a pair; PAIRED: both channels exist wherever the first does and
-// the address is aligned to the pair. `n` is the number of the pair's channels inside D.
-template <typename T, bool PAIRED>
+// Loads and stores of a lane's pair; VEC: both channels exist wherever the first does and
+// the address is aligned to the pair. `n`: channels of the pair inside D.
+template <typename T, bool VEC>
 __device__ __forceinline__ typename Pair<T>::Raw load_pair(const T* p, int n, typename Pair<T>::Raw none) {
   using P = Pair<T>;
-  if (PAIRED) return n ? __ldg(reinterpret_cast<const typename P::Raw*>(p)) : none;
+  if (VEC) return n ? __ldg(reinterpret_cast<const typename P::Raw*>(p)) : none;
   return n ? P::join(p[0], n > 1 ? p[1] : P::half(none, 1)) : none;
 }
-template <typename T, bool PAIRED>
+template <typename T, bool VEC>
 __device__ __forceinline__ void store_pair(T* p, int n, typename Pair<T>::Raw v) {
   using P = Pair<T>;
-  if (PAIRED) {
+  if (VEC) {
     if (n) *reinterpret_cast<typename P::Raw*>(p) = v;
   } else {
     if (n) p[0] = P::half(v, 0);
@@ -127,89 +128,157 @@ __device__ __forceinline__ void store_pair(T* p, int n, typename Pair<T>::Raw v)
   }
 }
 // f32 states [.., D]: 8-byte accesses where the pairs are aligned (D even)
-template <bool PAIRED>
+template <bool VEC>
 __device__ __forceinline__ uint64_t load_state(const float* p, int n) {
-  if (PAIRED) return n ? *reinterpret_cast<const uint64_t*>(p) : 0ull;
-  return f2_pack(n ? p[0] : 0.f, n > 1 ? p[1] : 0.f);
+  if (VEC) return n > 0 ? *reinterpret_cast<const uint64_t*>(p) : 0ull;
+  return f2_pack(n > 0 ? p[0] : 0.f, n > 1 ? p[1] : 0.f);
 }
-template <bool PAIRED>
+template <bool VEC>
 __device__ __forceinline__ void store_state(float* p, int n, uint64_t v) {
-  if (PAIRED) {
-    if (n) *reinterpret_cast<uint64_t*>(p) = v;
+  if (VEC) {
+    if (n > 0) *reinterpret_cast<uint64_t*>(p) = v;
   } else {
     const float2 f = f2_unpack(v);
-    if (n) p[0] = f.x;
+    if (n > 0) p[0] = f.x;
     if (n > 1) p[1] = f.y;
   }
 }
 
 // ---------------------------------------------------------------- the gate
-// log(1 + e) / e on [0, 1] and (e^{-s} - 1) / s on [0, 1]: Chebyshev expansions cut off
-// at degree 7 and 5 (relative errors 2.2e-7 and 8e-8, computed in 64 bits).
-__device__ __forceinline__ uint64_t log1p_over(uint64_t e) {
-  constexpr float k[8] = {0.999999762f, -0.499971271f, 0.332711875f, -0.244704694f, 0.176754937f, -0.106677905f, 0.0433708504f, -0.00833649747f};
-  uint64_t r = f2_both(k[7]);
+// log(1 + e) / e on [0, 1]: a Chebyshev expansion cut off at degree 7 (relative error 2.4e-7,
+// computed in 64 bits). Both halves of the packed operands stand in constant memory.
+__constant__ float2 kLog1p[8] = {
+    {0.999999762f, 0.999999762f},   {-0.499971271f, -0.499971271f}, {0.332711875f, 0.332711875f},
+    {-0.244704694f, -0.244704694f}, {0.176754937f, 0.176754937f},   {-0.106677905f, -0.106677905f},
+    {0.0433708504f, 0.0433708504f}, {-0.00833649747f, -0.00833649747f}};
+__device__ __forceinline__ uint64_t f2_const(const float2& v) { return *reinterpret_cast<const uint64_t*>(&v); }
+// softplus(-z) of K pairs. The K are taken through every operation together: one pair's
+// operations wait for each other, and a scheduler has four warps to fill the gaps.
+template <int K>
+__device__ __forceinline__ void softplus_neg(const uint64_t (&z)[K], uint64_t (&s)[K]) {
+  uint64_t e[K];
 #pragma unroll
-  for (int i = 6; i >= 0; --i) r = f2_fma(r, e, f2_both(k[i]));
-  return r;
+  for (int k = 0; k < K; ++k) {
+    const float2 f = f2_unpack(z[k]);
+    e[k] = f2_pack(ex2_approx(-kLog2e * fabsf(f.x)), ex2_approx(-kLog2e * fabsf(f.y)));
+  }
+#pragma unroll
+  for (int k = 0; k < K; ++k) s[k] = f2_const(kLog1p[7]);
+#pragma unroll
+  for (int i = 6; i >= 0; --i)
+#pragma unroll
+    for (int k = 0; k < K; ++k) s[k] = f2_fma(s[k], e[k], f2_const(kLog1p[i]));
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const float2 f = f2_unpack(z[k]);
+    s[k] = f2_fma(e[k], s[k], f2_pack(fmaxf(-f.x, 0.f), fmaxf(-f.y, 0.f)));
+  }
 }
-__device__ __forceinline__ uint64_t expm1_over(uint64_t s) {
-  constexpr float k[6] = {-0.99999994f, 0.499994457f, -0.16660437f, 0.0414042994f, -0.00782115851f, 0.000906161731f};
-  uint64_t r = f2_both(k[5]);
+// e^{-S / tau} - 1 of K pairs by the expansion
+template <int K>
+__device__ __forceinline__ void expm1_small(const uint64_t (&s)[K], const DecayParams& g, uint64_t (&r)[K]) {
 #pragma unroll
-  for (int i = 4; i >= 0; --i) r = f2_fma(r, s, f2_both(k[i]));
-  return r;
+  for (int k = 0; k < K; ++k) r[k] = f2_const(g.expm1[4]);
+#pragma unroll
+  for (int i = 3; i >= 0; --i)
+#pragma unroll
+    for (int k = 0; k < K; ++k) r[k] = f2_fma(r[k], s[k], f2_const(g.expm1[i]));
+#pragma unroll
+  for (int k = 0; k < K; ++k) r[k] = f2_mul(s[k], r[k]);
 }
 
-// -c of two logits, and with DOWN also a (1 - sigmoid(z)) / tau. For f32 tensors the
-// library functions: their callers compare 24 bits, and 12 bytes an element leave time.
-// TAU1: c = 1 - sigmoid(z) in closed form, one ex2 and one reciprocal.
-template <typename T, bool TAU1, bool DOWN>
-__device__ __forceinline__ uint64_t neg_decay(uint64_t z, float inv_tau, uint64_t& down) {
-  const float2 f = f2_unpack(z);
-  if constexpr (sizeof(T) == 4) {
-    float nc[2], d[2];
+// Whether -c comes from the expansion, and so has a `far` to look at.
+template <typename T, bool TAU1>
+constexpr bool kExpansion = sizeof(T) == 2 && !TAU1;
+
+// -c of K pairs of logits. With S = softplus(-z), -c = e^{-S / tau} - 1 is S times a
+// polynomial in S while S <= tau / 2; `far` takes the largest S of the calls, beyond that bound
+// neg_decay_far has to be called. For f32 tensors the library functions: their callers
+// compare 24 bits, and 12 bytes an element leave time. TAU1: c = 1 - sigmoid(z) in closed form.
+template <typename T, bool TAU1, int K>
+__device__ __forceinline__ void neg_decay(const uint64_t (&z)[K], const DecayParams& g, float& far, uint64_t (&nc)[K]) {
+  if constexpr (kExpansion<T, TAU1>) {
+    uint64_t s[K];
+    softplus_neg(z, s);
+    expm1_small(s, g, nc);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float v = i ? f.y : f.x, e = expf(-fabsf(v));
-      const float dn = (v >= 0.f ? e : 1.f) / (1.f + e);
-      nc[i] = TAU1 ? -dn : expm1f(-(log1pf(e) + fmaxf(-v, 0.f)) * inv_tau);
-      if (DOWN) d[i] = dn * (1.f + nc[i]) * inv_tau;
+    for (int k = 0; k < K; ++k) {
+      const float2 f = f2_unpack(s[k]);
+      far = fmaxf(far, fmaxf(f.x, f.y));
     }
-    if (DOWN) down = f2_pack(d[0], d[1]);
-    return f2_pack(nc[0], nc[1]);
   } else {
-    const float e0 = ex2_approx(-kLog2e * fabsf(f.x)), e1 = ex2_approx(-kLog2e * fabsf(f.y));
-    float d0, d1;
-    if (TAU1 || DOWN) {
-      d0 = (f.x >= 0.f ? e0 : 1.f) * rcp_approx(1.f + e0);
-      d1 = (f.y >= 0.f ? e1 : 1.f) * rcp_approx(1.f + e1);
-    }
-    uint64_t nc;
-    if (TAU1) {
-      nc = f2_pack(-d0, -d1);
-    } else {
-      const uint64_t e = f2_pack(e0, e1);
-      uint64_t s = f2_fma(e, log1p_over(e), f2_pack(fmaxf(-f.x, 0.f), fmaxf(-f.y, 0.f)));
-      s = f2_mul(s, f2_both(inv_tau));
-      nc = f2_mul(s, expm1_over(s));
-      const float2 sf = f2_unpack(s);
-      if (fmaxf(sf.x, sf.y) > 1.f) {  // outside the expansion's interval; e^{-s} < 0.37 loses nothing in the difference
-        float2 n = f2_unpack(nc);
-        if (sf.x > 1.f) n.x = ex2_approx(-kLog2e * sf.x) - 1.f;
-        if (sf.y > 1.f) n.y = ex2_approx(-kLog2e * sf.y) - 1.f;
-        nc = f2_pack(n.x, n.y);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const float2 f = f2_unpack(z[k]);
+      float v[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float u = i ? f.y : f.x;
+        if constexpr (sizeof(T) == 4) {
+          const float e = expf(-fabsf(u));
+          v[i] = TAU1 ? -(u >= 0.f ? e : 1.f) / (1.f + e) : expm1f(-(log1pf(e) + fmaxf(-u, 0.f)) * g.inv_tau);
+        } else {
+          const float e = ex2_approx(-kLog2e * fabsf(u));
+          v[i] = -(u >= 0.f ? e : 1.f) * rcp_approx(1.f + e);
+        }
       }
+      nc[k] = f2_pack(v[0], v[1]);
     }
-    if (DOWN) down = f2_mul(f2_mul(f2_pack(d0, d1), f2_both(inv_tau)), f2_add(nc, f2_both(1.f)));
-    return nc;
+  }
+}
+// -c where S may be large: e^{-S / tau} < 0.61 loses nothing in the difference from one.
+__device__ __forceinline__ uint64_t neg_decay_far(uint64_t z, const DecayParams& g) {
+  uint64_t zz[1] = {z}, s[1], r[1];
+  softplus_neg(zz, s);
+  expm1_small(s, g, r);
+  const float2 sf = f2_unpack(s[0]);
+  float2 n = f2_unpack(r[0]);
+  if (sf.x > g.far) n.x = ex2_approx(-kLog2e * g.inv_tau * sf.x) - 1.f;
+  if (sf.y > g.far) n.y = ex2_approx(-kLog2e * g.inv_tau * sf.y) - 1.f;
+  return f2_pack(n.x, n.y);
+}
+
+// -c of a warp's R rows of logits in shared memory, K pairs at a time.
+template <typename T, bool TAU1, int R>
+__device__ __forceinline__ void row_decays(const typename Pair<T>::Raw* zs, const DecayParams& g, uint64_t (&nc)[R]) {
+  using P = Pair<T>;
+  constexpr int K = kExpansion<T, TAU1> ? 4 : 2;
+  float far = 0.f;
+#pragma unroll
+  for (int r = 0; r < R; r += K) {
+    uint64_t z[K], v[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) z[k] = P::f32(zs[(r + k) * 32]);
+    neg_decay<T, TAU1>(z, g, far, v);
+#pragma unroll
+    for (int k = 0; k < K; ++k) nc[r + k] = v[k];
+  }
+  if (kExpansion<T, TAU1> && far > g.far) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) nc[r] = neg_decay_far(P::f32(zs[r * 32]), g);
   }
 }
 
+// a (1 - sigmoid(z)) / tau, for padded rows (z = +inf, c = 0) zero
+template <typename T>
+__device__ __forceinline__ uint64_t decay_slope(uint64_t z, uint64_t nc, float inv_tau) {
+  const float2 f = f2_unpack(z);
+  float2 d;
+  if constexpr (sizeof(T) == 4) {
+    const float e0 = expf(-fabsf(f.x)), e1 = expf(-fabsf(f.y));
+    d = make_float2((f.x >= 0.f ? e0 : 1.f) / (1.f + e0), (f.y >= 0.f ? e1 : 1.f) / (1.f + e1));
+  } else {
+    const float e0 = ex2_approx(-kLog2e * fabsf(f.x)), e1 = ex2_approx(-kLog2e * fabsf(f.y));
+    d = make_float2((f.x >= 0.f ? e0 : 1.f) * rcp_approx(1.f + e0), (f.y >= 0.f ? e1 : 1.f) * rcp_approx(1.f + e1));
+  }
+  return f2_mul(f2_mul(f2_pack(d.x, d.y), f2_both(inv_tau)), f2_add(nc, f2_both(1.f)));
+}
+
 // h - c h + u
-__device__ __forceinline__ uint64_t advance(uint64_t h, uint64_t nc, uint64_t x, bool tied) {
+template <bool TIED>
+__device__ __forceinline__ uint64_t advance(uint64_t h, uint64_t nc, uint64_t x) {
   h = f2_fma(nc, h, h);
-  return tied ? f2_fma(nc, f2_neg(x), h) : f2_add(h, x);
+  return TIED ? f2_fma(nc, f2_neg(x), h) : f2_add(h, x);
 }
 
 // ---------------------------------------------------------------- blocks and clusters
@@ -218,14 +287,19 @@ struct alignas(16) Join {
   uint64_t p, v;
 };
 
-// Sends this block's pair to every block of the cluster and waits for all of them.
+// Sends this block's joins to every block of the cluster and waits for theirs. What the
+// other warps read of the slots two steps ago is ordered before the sender's release by
+// the block barrier between, so they need not release anything themselves.
 __device__ __forceinline__ void send_join(Join* slots, int rank, int cluster, const Join& j, bool sender) {
   if (sender) {
     const uint32_t at = smem_u32(slots + rank * 32 + lane_id());
     for (int r = 0; r < cluster; ++r)
       asm volatile("st.shared::cluster.v2.b64 [%0], {%1, %2};" ::"r"(mapa_shared(at, r)), "l"(j.p), "l"(j.v) : "memory");
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  } else {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   }
-  cluster_sync();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // Bits of the valid rows t0 .. t0 + R - 1 (bit r: row t0 + r).
@@ -237,227 +311,526 @@ __device__ __forceinline__ uint32_t valid_rows(const uint8_t* m, int t0, int L) 
   return __ballot_sync(~0u, r < n && m[t0 + r] != 0);
 }
 
+// ---------------------------------------------------------------- rows in shared memory
+// A warp's R rows of 64 channels take 2 KB for every type (16 rows of 128 bytes, 8 of 256).
+constexpr int kRowsBytes = 2048;
+template <typename T>
+constexpr int kRowsOf = kRowsBytes / (64 * sizeof(T));
+
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Starts a warp's copy of rows t0 .. t0 + R - 1 of channels c0 .. c0 + 63 to `to`; rows whose bit
+// is not set and channels past D become `none`. VEC: 16-byte copies (rows aligned to 16
+// bytes and D a whole number of them); else the lanes load and store their pairs at once.
+template <typename T, bool VEC, int R = kRowsOf<T>>
+__device__ __forceinline__ void fetch(uint8_t* to, const Rows& r, int b, int t0, int c0, int D, uint32_t bits,
+                                      typename Pair<T>::Raw none) {
+  constexpr int kRow = 64 * sizeof(T), kEach = 512 / kRow;
+  const int lane = lane_id();
+  const T* base = static_cast<const T*>(r.ptr) + b * r.batch + static_cast<long long>(t0) * r.row + c0;
+  if constexpr (VEC) {
+    const int row = lane * 16 / kRow, col = lane * 16 % kRow;
+    const bool inside = c0 + col / static_cast<int>(sizeof(T)) < D;
+    const T* from = base + row * r.row + col / sizeof(T);
+    const uint32_t at = smem_u32(to) + lane * 16;
+    bits >>= row;
+#pragma unroll
+    for (int i = 0; i < R / kEach; ++i, from += kEach * r.row) {
+      if (inside && (bits >> i * kEach & 1)) {
+        copy16(at + i * 512, from);
+      } else {
+        uint32_t v = static_cast<uint32_t>(none);  // the halves of a 64-bit pair are alike
+        st_shared_v4(at + i * 512, v, v, v, v);
+      }
+    }
+  } else {
+    const int n = min(max(D - c0 - 2 * lane, 0), 2);
+#pragma unroll 4
+    for (int i = 0; i < R; ++i)
+      reinterpret_cast<typename Pair<T>::Raw*>(to + i * kRow)[lane] =
+          load_pair<T, false>(base + i * r.row + 2 * lane, bits >> i & 1 ? n : 0, none);
+  }
+}
+
+// Stores a warp's rows t0 .. from shared memory; rows whose bit is not set as zeros.
+template <typename T, bool VEC, int R = kRowsOf<T>>
+__device__ __forceinline__ void put(const uint8_t* from, const Rows& r, int b, int t0, int c0, int D, int L, uint32_t bits) {
+  constexpr int kRow = 64 * sizeof(T), kEach = 512 / kRow;
+  const int lane = lane_id();
+  T* base = static_cast<T*>(r.ptr) + b * r.batch + static_cast<long long>(t0) * r.row + c0;
+  if constexpr (VEC) {
+    const int row = lane * 16 / kRow, col = lane * 16 % kRow;
+    const int last = c0 + col / static_cast<int>(sizeof(T)) < D ? L - t0 - row : 0;
+    T* to = base + row * r.row + col / sizeof(T);
+    bits >>= row;
+#pragma unroll
+    for (int i = 0; i < R / kEach; ++i, to += kEach * r.row) {
+      uint4 v = reinterpret_cast<const uint4*>(from)[i * 32 + lane];
+      if (!(bits >> i * kEach & 1)) v = make_uint4(0, 0, 0, 0);
+      if (i * kEach < last) *reinterpret_cast<uint4*>(to) = v;
+    }
+  } else {
+    using Raw = typename Pair<T>::Raw;
+    const int n = min(max(D - c0 - 2 * lane, 0), 2);
+#pragma unroll 4
+    for (int i = 0; i < R; ++i)
+      if (t0 + i < L)
+        store_pair<T, false>(base + i * r.row + 2 * lane, n,
+                             bits >> i & 1 ? reinterpret_cast<const Raw*>(from + i * kRow)[lane] : Pair<T>::zero());
+  }
+}
+
 // ---------------------------------------------------------------- forward
-template <typename T, int W, int R, bool PAIRED, bool TAU1>
-__global__ void __launch_bounds__(W * 32, W == 8 ? 2 : 1) scan_forward_kernel(const ScanParams p) {
+constexpr int kWarps = 8;
+constexpr int kForwardStages = 2;  // steps of rows in shared memory: one used, one on its way
+constexpr int kForwardRows = kWarps * kForwardStages * 2 * kRowsBytes;
+constexpr int kSlots = 2 * 32 * sizeof(Join);  // what one block of a cluster sends, double-buffered
+
+template <typename T, bool VEC, bool TAU1, bool TIED>
+__global__ void __launch_bounds__(kWarps * 32, 3) scan_forward_kernel(const ScanParams p) {
   using P = Pair<T>;
   using Raw = typename P::Raw;
-  constexpr int kRows = W * R;
-  static_assert(R <= 32 && kScanSave % R == 0, "saved states start a warp's rows");
-  __shared__ Join warps[W][32];
-  __shared__ Join blocks[2][kMaxCluster * 32];
+  constexpr int R = kRowsOf<T>, kRows = kWarps * R, kStages = kForwardStages;
+  extern __shared__ __align__(128) uint8_t dynamic[];
+  __shared__ Join warps[2][kWarps][32];
   const int cluster = p.cluster, rank = cluster > 1 ? cluster_ctarank() : 0;
   const int w = warp_id(), lane = lane_id(), b = blockIdx.y;
-  const int ch = blockIdx.x / cluster * kTile + 2 * lane, n = min(max(p.D - ch, 0), 2);
-  const bool tied = p.tied;
-  const T* x = static_cast<const T*>(p.x.ptr) + b * p.x.batch + ch;
-  const T* z = static_cast<const T*>(p.z.ptr) + b * p.z.batch + ch;
-  T* o = static_cast<T*>(p.h.ptr) + b * p.h.batch + ch;
+  const int c0 = blockIdx.x / cluster * 64, ch = c0 + 2 * lane, n = min(max(p.D - ch, 0), 2);
+  uint8_t* mine = dynamic + w * kStages * 2 * kRowsBytes;
   const uint8_t* m = p.mask ? p.mask + static_cast<size_t>(b) * p.L : nullptr;
   const size_t state_at = static_cast<size_t>(b) * p.D + ch;
-  const int nsave = (p.L + kScanSave - 1) / kScanSave;
-  const int steps = (p.L + cluster * kRows - 1) / (cluster * kRows);
+  const int chunks = (p.L + R - 1) / R, steps = (p.L + cluster * kRows - 1) / (cluster * kRows);
 
-  Raw xr[R], zr[R];
-  uint32_t bits;
-  auto load = [&](int t0) {
-    bits = valid_rows<R>(m, t0, p.L);
-    const T* xp = x + static_cast<long long>(t0) * p.x.row;
-    const T* zp = z + static_cast<long long>(t0) * p.z.row;
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int k = bits >> r & 1 ? n : 0;
-      xr[r] = load_pair<T, PAIRED>(xp + r * p.x.row, k, P::zero());
-      zr[r] = load_pair<T, PAIRED>(zp + r * p.z.row, k, P::inf());
+  uint32_t coming;  // valid rows on their way
+  auto start_step = [&](int step) {
+    if (step < steps) {
+      const int t0 = ((step * cluster + rank) * kWarps + w) * R;
+      uint8_t* to = mine + step % kStages * 2 * kRowsBytes;
+      coming = valid_rows<R>(m, t0, p.L);
+      fetch<T, VEC>(to, p.x, b, t0, c0, p.D, coming, P::zero());
+      fetch<T, VEC>(to + kRowsBytes, p.z, b, t0, c0, p.D, coming, P::inf());
     }
+    copies_commit();
   };
 
-  uint64_t carry = p.h0 ? load_state<PAIRED>(p.h0 + state_at, n) : 0ull;
-  load((rank * W + w) * R);
+  start_step(0);
+  uint64_t carry = p.h0 ? load_state<VEC>(p.h0 + state_at, n) : 0ull;
   if (cluster > 1) cluster_sync();  // every block runs before another writes to it
   for (int step = 0; step < steps; ++step) {
-    const int t0 = ((step * cluster + rank) * W + w) * R;
-    uint64_t nc[R], unused, prod = f2_both(1.f), h = 0ull;
-    Raw xs[R];
-    const uint32_t now = bits;
+    const int t0 = ((step * cluster + rank) * kWarps + w) * R;
+    const uint32_t now = coming;
+    __syncwarp();  // the lanes have read what the next copy overwrites
+    start_step(step + 1);
+    copies_wait<1>();
+    __syncwarp();
+    uint8_t* rows = mine + step % kStages * 2 * kRowsBytes;
+    Raw* xs = reinterpret_cast<Raw*>(rows) + lane;
+    const Raw* zs = xs + kRowsBytes / sizeof(Raw);
+    uint64_t nc[R];
+    row_decays<T, TAU1>(zs, p.gate, nc);
+    Join join{f2_both(1.f), 0ull};
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      xs[r] = xr[r];
-      nc[r] = neg_decay<T, TAU1, false>(P::f32(zr[r]), p.inv_tau, unused);
+      join.v = advance<TIED>(join.v, nc[r], P::f32(xs[r * 32]));
+      join.p = f2_fma(nc[r], join.p, join.p);
     }
-    if (step + 1 < steps) load(t0 + cluster * kRows);
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      h = advance(h, nc[r], P::f32(xs[r]), tied);
-      prod = f2_fma(nc[r], prod, prod);
-    }
-    warps[w][lane] = Join{prod, h};
+    Join(*wj)[32] = warps[step & 1];
+    wj[w][lane] = join;
     __syncthreads();
-    Join before{f2_both(1.f), 0ull}, all{f2_both(1.f), 0ull};
+    uint64_t h = carry;
+    if (cluster == 1) {
 #pragma unroll
-    for (int j = 0; j < W; ++j) {
-      if (j == w) before = all;
-      const Join q = warps[j][lane];
-      all.v = f2_fma(q.p, all.v, q.v);
-      all.p = f2_mul(q.p, all.p);
-    }
-    uint64_t start = carry;
-    if (cluster > 1) {
-      Join* slots = blocks[step & 1];
-      send_join(slots, rank, cluster, all, w == 0);
-      for (int j = 0; j < cluster; ++j) {
-        if (j == rank) start = carry;
-        const Join q = slots[j * 32 + lane];
+      for (int j = 0; j < kWarps; ++j) {
+        if (j == w) h = carry;
+        const Join q = wj[j][lane];
         carry = f2_fma(q.p, carry, q.v);
       }
     } else {
-      carry = f2_fma(all.p, carry, all.v);
-      __syncthreads();  // the next step writes `warps`
+      Join before{f2_both(1.f), 0ull}, all{f2_both(1.f), 0ull};
+#pragma unroll
+      for (int j = 0; j < kWarps; ++j) {
+        if (j == w) before = all;
+        const Join q = wj[j][lane];
+        all.v = f2_fma(q.p, all.v, q.v);
+        all.p = f2_mul(q.p, all.p);
+      }
+      Join* slots = reinterpret_cast<Join*>(dynamic + kForwardRows) + (step & 1) * cluster * 32;
+      send_join(slots, rank, cluster, all, w == 0);
+      for (int j = 0; j < cluster; ++j) {
+        if (j == rank) h = carry;
+        const Join q = slots[j * 32 + lane];
+        carry = f2_fma(q.p, carry, q.v);
+      }
+      h = f2_fma(before.p, h, before.v);
     }
-    h = f2_fma(before.p, start, before.v);
-    if (p.saved && t0 % kScanSave == 0 && t0 < p.L)
-      store_state<PAIRED>(p.saved + (static_cast<size_t>(b) * nsave + t0 / kScanSave) * p.D + ch, n, h);
-    T* op = o + static_cast<long long>(t0) * p.h.row;
+    if (p.saved && t0 < p.L) store_state<VEC>(p.saved + (static_cast<size_t>(b) * chunks + t0 / R) * p.D + ch, n, h);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      h = advance(h, nc[r], P::f32(xs[r]), tied);
-      if (t0 + r < p.L) store_pair<T, PAIRED>(op + r * p.h.row, n, now >> r & 1 ? P::round(h) : P::zero());
+      h = advance<TIED>(h, nc[r], P::f32(xs[r * 32]));
+      xs[r * 32] = P::round(h);
     }
+    __syncwarp();
+    put<T, VEC>(rows, p.h, b, t0, c0, p.D, p.L, now);
   }
-  if (rank == 0 && w == 0) store_state<PAIRED>(p.last + state_at, n, carry);
+  if (rank == 0 && w == 0) store_state<VEC>(p.last + state_at, n, carry);
+}
+
+// ---------------------------------------------------------------- forward, one chain per tile
+// Groups of two warps load chunks and turn their logits into -c, one warp walks through the
+// chunks in order: h takes the place of x, and the group stores it. Named barriers of
+// the group's and the chain's threads hand a chunk over and back.
+constexpr int kGroups = 7, kGroupWarps = 2;
+constexpr int kMeeting = 32 * kGroupWarps + 32;
+constexpr int kChainThreads = kGroups * kGroupWarps * 32 + 32;
+__device__ __forceinline__ void meet(int id) { asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(kMeeting) : "memory"); }
+__device__ __forceinline__ void leave(int id) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "n"(kMeeting) : "memory"); }
+
+constexpr int kRing = 3;  // chunks of a group in shared memory: one used, two on their way
+constexpr int kNcBytes = 2 * kRowsBytes;  // -c of a chunk as f32 (f32 tensors use half of it)
+constexpr int kChainGroup = kRing * 2 * kRowsBytes + kNcBytes;
+constexpr int kChainShared = kGroups * kChainGroup;
+
+template <typename T, bool VEC, bool TAU1, bool TIED>
+__global__ void __launch_bounds__(kChainThreads, 2) scan_chain_kernel(const ScanParams p) {
+  using P = Pair<T>;
+  using Raw = typename P::Raw;
+  constexpr int R = kRowsOf<T>, RW = R / kGroupWarps, kRowsHere = RW * 64 * sizeof(T);
+  extern __shared__ __align__(128) uint8_t dynamic[];
+  const int w = warp_id(), lane = lane_id(), b = blockIdx.y, c0 = blockIdx.x * 64;
+  const int chunks = (p.L + R - 1) / R;
+  if (w < kGroups * kGroupWarps) {
+    const int g = w / kGroupWarps, r0 = w % kGroupWarps * RW;  // this warp's rows of a chunk
+    uint8_t* mine = dynamic + g * kChainGroup + w % kGroupWarps * kRowsHere;
+    uint64_t* ncs = reinterpret_cast<uint64_t*>(dynamic + g * kChainGroup + kRing * 2 * kRowsBytes) + r0 * 32 + lane;
+    const uint8_t* m = p.mask ? p.mask + static_cast<size_t>(b) * p.L : nullptr;
+    auto start = [&](int c, int slot) {
+      uint32_t bits = 0;
+      if (c < chunks) {
+        bits = valid_rows<RW>(m, c * R + r0, p.L);
+        uint8_t* to = mine + slot * 2 * kRowsBytes;
+        fetch<T, VEC, RW>(to, p.x, b, c * R + r0, c0, p.D, bits, P::zero());
+        fetch<T, VEC, RW>(to + kRowsBytes, p.z, b, c * R + r0, c0, p.D, bits, P::inf());
+      }
+      copies_commit();
+      return bits;
+    };
+    uint32_t before = 0, now = start(g, 0), next = start(g + kGroups, 1);
+    int slot = 0;
+    for (int c = g; c < chunks + kGroups; c += kGroups) {
+      const int last = slot == 0 ? kRing - 1 : slot - 1;
+      if (c >= kGroups) meet(8 + g);  // the chain has been through the chunk before
+      if (c < chunks) {
+        copies_wait<1>();
+        __syncwarp();
+        const Raw* zs = reinterpret_cast<const Raw*>(mine + (slot * 2 + 1) * kRowsBytes) + lane;
+        uint64_t nc[RW];
+        row_decays<T, TAU1>(zs, p.gate, nc);
+#pragma unroll
+        for (int r = 0; r < RW; ++r) ncs[r * 32] = nc[r];
+        leave(1 + g);
+      }
+      if (c >= kGroups)
+        put<T, VEC, RW>(mine + last * 2 * kRowsBytes, p.h, b, (c - kGroups) * R + r0, c0, p.D, p.L, before);
+      __syncwarp();
+      before = now;
+      now = next;
+      next = start(c + 2 * kGroups, last);
+      slot = slot + 1 == kRing ? 0 : slot + 1;
+    }
+  } else {
+    const int ch = c0 + 2 * lane, n = min(max(p.D - ch, 0), 2);
+    const size_t state_at = static_cast<size_t>(b) * p.D + ch;
+    float* saved = p.saved ? p.saved + static_cast<size_t>(b) * chunks * p.D + ch : nullptr;
+    uint64_t h = p.h0 ? load_state<VEC>(p.h0 + state_at, n) : 0ull;
+    int group = 0, slot = 0;
+    for (int c = 0; c < chunks; ++c) {
+      if (saved) store_state<VEC>(saved + static_cast<size_t>(c) * p.D, n, h);
+      uint8_t* his = dynamic + group * kChainGroup;
+      Raw* xs = reinterpret_cast<Raw*>(his + slot * 2 * kRowsBytes) + lane;
+      const uint64_t* ncs = reinterpret_cast<const uint64_t*>(his + kRing * 2 * kRowsBytes) + lane;
+      meet(1 + group);
+#pragma unroll
+      for (int half = 0; half < R; half += 8) {
+        uint64_t nc[8];
+        Raw x[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          nc[r] = ncs[(half + r) * 32];
+          x[r] = xs[(half + r) * 32];
+        }
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          h = advance<TIED>(h, nc[r], P::f32(x[r]));
+          xs[(half + r) * 32] = P::round(h);
+        }
+      }
+      leave(8 + group);
+      if (++group == kGroups) {
+        group = 0;
+        slot = slot + 1 == kRing ? 0 : slot + 1;
+      }
+    }
+    store_state<VEC>(p.last + state_at, n, h);
+  }
 }
 
 // ---------------------------------------------------------------- backward
-// Blocks of 64 rows, from the last: rank 0 of a cluster takes the latest. A warp's rows
-// hand a_t g_t of their first row down to the rows before: in = P out + G.
-template <typename T, int W, int R, bool PAIRED, bool TAU1>
-__global__ void __launch_bounds__(W * 32, W == 8 ? 2 : 1) scan_backward_kernel(const ScanParams p) {
+// Chunks of R rows, from the last. A chunk's states are rebuilt from its saved one, so
+// everything but g is independent of the other chunks: per row -c and
+// q = (h_{t-1} - [tied] x_t) a_t (1 - sigmoid(z_t)) / tau. Then, down the rows,
+// g_t = dh_t + in, dz_t = g_t q_t, in = a_t g_t.
+template <typename T, bool TAU1, bool TIED>
+__device__ __forceinline__ void row_factors(const typename Pair<T>::Raw* xs, const typename Pair<T>::Raw* zs, uint64_t h,
+                                            const DecayParams& gate, uint64_t (&nc)[kRowsOf<T>],
+                                            uint64_t (&q)[kRowsOf<T>]) {
+  using P = Pair<T>;
+  constexpr int R = kRowsOf<T>;
+  row_decays<T, TAU1>(zs, gate, nc);
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const uint64_t x = P::f32(xs[r * 32]);
+    q[r] = f2_mul(TIED ? f2_add(h, f2_neg(x)) : h, decay_slope<T>(P::f32(zs[r * 32]), nc[r], gate.inv_tau));
+    h = advance<TIED>(h, nc[r], x);
+  }
+}
+template <bool TIED>
+__device__ __forceinline__ uint64_t input_grad(uint64_t nc, uint64_t g) {
+  return TIED ? f2_neg(f2_mul(nc, g)) : g;
+}
+
+// One chain per tile: workers make -c and q in shared memory, the chain warp walks down.
+// -c takes the place of x and z, then dx and dz do.
+constexpr int kWorkers = 7;
+__device__ __forceinline__ void meet_one(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ void leave_one(int id) { asm volatile("bar.arrive %0, 64;" ::"r"(id) : "memory"); }
+constexpr int kBackRing = 2;
+constexpr int kBackWorker = kBackRing * 3 * kRowsBytes + kNcBytes;
+constexpr int kBackShared = kWorkers * kBackWorker;
+
+template <typename T>
+__device__ __forceinline__ void put_nc(typename Pair<T>::Raw* xs, typename Pair<T>::Raw* zs, uint64_t v) {
+  if constexpr (sizeof(T) == 4) {
+    *zs = v;
+  } else {
+    const float2 f = f2_unpack(v);
+    *xs = __float_as_uint(f.x);
+    *zs = __float_as_uint(f.y);
+  }
+}
+template <typename T>
+__device__ __forceinline__ uint64_t get_nc(const typename Pair<T>::Raw* xs, const typename Pair<T>::Raw* zs) {
+  if constexpr (sizeof(T) == 4) return *zs;
+  else return f2_pack(__uint_as_float(*xs), __uint_as_float(*zs));
+}
+
+template <typename T, bool VEC, bool TAU1, bool TIED>
+__global__ void __launch_bounds__(kWorkers * 32 + 32, 2) scan_chain_backward_kernel(const ScanParams p) {
   using P = Pair<T>;
   using Raw = typename P::Raw;
-  static_assert(W * R == kScanSave, "a block's rows start from a saved state");
-  __shared__ Join warps[W][32];
-  __shared__ uint64_t grads[W][32];
-  __shared__ Join blocks[2][kMaxCluster * 32];
+  constexpr int R = kRowsOf<T>;
+  extern __shared__ __align__(128) uint8_t dynamic[];
+  const int w = warp_id(), lane = lane_id(), b = blockIdx.y, c0 = blockIdx.x * 64;
+  const int ch = c0 + 2 * lane, n = min(max(p.D - ch, 0), 2);
+  const int chunks = (p.L + R - 1) / R;
+  if (w < kWorkers) {
+    uint8_t* mine = dynamic + w * kBackWorker;
+    uint64_t* qs = reinterpret_cast<uint64_t*>(mine + kBackRing * 3 * kRowsBytes) + lane;
+    const uint8_t* m = p.mask ? p.mask + static_cast<size_t>(b) * p.L : nullptr;
+    const float* saved = p.saved + static_cast<size_t>(b) * chunks * p.D + ch;
+    uint64_t state = 0ull;
+    auto start = [&](int k, int slot) {  // the chunk k from the end
+      uint32_t bits = 0;
+      if (k < chunks) {
+        const int c = chunks - 1 - k;
+        bits = valid_rows<R>(m, c * R, p.L);
+        uint8_t* to = mine + slot * 3 * kRowsBytes;
+        fetch<T, VEC>(to, p.x, b, c * R, c0, p.D, bits, P::zero());
+        fetch<T, VEC>(to + kRowsBytes, p.z, b, c * R, c0, p.D, bits, P::inf());
+        fetch<T, VEC>(to + 2 * kRowsBytes, p.dh, b, c * R, c0, p.D, p.dh.ptr ? bits : 0u, P::zero());
+        state = load_state<VEC>(saved + static_cast<size_t>(c) * p.D, n);
+      }
+      copies_commit();
+      return bits;
+    };
+    uint32_t before = 0, now = start(w, 0);
+    int slot = 0;
+    for (int k = w; k < chunks + kWorkers; k += kWorkers, slot ^= 1) {
+      if (k < chunks) copies_wait<0>();
+      if (k >= kWorkers) meet_one(8 + w);
+      __syncwarp();
+      if (k < chunks) {
+        Raw* xs = reinterpret_cast<Raw*>(mine + slot * 3 * kRowsBytes) + lane;
+        Raw* zs = xs + kRowsBytes / sizeof(Raw);
+        uint64_t nc[R], q[R];
+        row_factors<T, TAU1, TIED>(xs, zs, state, p.gate, nc, q);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          put_nc<T>(xs + r * 32, zs + r * 32, nc[r]);
+          qs[r * 32] = q[r];
+        }
+        leave_one(1 + w);
+      }
+      if (k >= kWorkers) {
+        const uint8_t* done = mine + (slot ^ 1) * 3 * kRowsBytes;
+        const int t0 = (chunks - 1 - (k - kWorkers)) * R;
+        put<T, VEC>(done, p.dx, b, t0, c0, p.D, p.L, before);
+        put<T, VEC>(done + kRowsBytes, p.dz, b, t0, c0, p.D, p.L, before);
+      }
+      __syncwarp();
+      before = now;
+      now = start(k + kWorkers, slot ^ 1);
+    }
+  } else {
+    const size_t state_at = static_cast<size_t>(b) * p.D + ch;
+    uint64_t in = p.dlast ? load_state<VEC>(p.dlast + state_at, n) : 0ull;
+    int worker = 0, slot = 0;
+    for (int k = 0; k < chunks; ++k) {
+      uint8_t* his = dynamic + worker * kBackWorker;
+      Raw* xs = reinterpret_cast<Raw*>(his + slot * 3 * kRowsBytes) + lane;
+      Raw* zs = xs + kRowsBytes / sizeof(Raw);
+      const Raw* ds = zs + kRowsBytes / sizeof(Raw);
+      const uint64_t* qs = reinterpret_cast<const uint64_t*>(his + kBackRing * 3 * kRowsBytes) + lane;
+      meet_one(1 + worker);
+      uint64_t nc[R], q[R];
+      Raw d[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        nc[r] = get_nc<T>(xs + r * 32, zs + r * 32);
+        q[r] = qs[r * 32];
+        d[r] = ds[r * 32];
+      }
+#pragma unroll
+      for (int r = R - 1; r >= 0; --r) {
+        const uint64_t g = f2_add(in, P::f32(d[r]));
+        in = f2_fma(nc[r], g, g);
+        xs[r * 32] = P::round(input_grad<TIED>(nc[r], g));
+        zs[r * 32] = P::round(f2_mul(g, q[r]));
+      }
+      leave_one(8 + worker);
+      if (++worker == kWorkers) {
+        worker = 0;
+        slot ^= 1;
+      }
+    }
+    if (p.dh0) store_state<VEC>(p.dh0 + state_at, n, in);
+  }
+}
+
+// Rows split over a cluster: rank 0 and its warp 0 take the latest chunks. A chunk hands
+// down out = P in + G.
+constexpr int kBackRows = kWarps * 2 * 3 * kRowsBytes;
+
+template <typename T, bool VEC, bool TAU1, bool TIED>
+__global__ void __launch_bounds__(kWarps * 32, 2) scan_backward_kernel(const ScanParams p) {
+  using P = Pair<T>;
+  using Raw = typename P::Raw;
+  constexpr int R = kRowsOf<T>;
+  extern __shared__ __align__(128) uint8_t dynamic[];
+  __shared__ Join warps[2][kWarps][32];
   const int cluster = p.cluster, rank = cluster > 1 ? cluster_ctarank() : 0;
   const int w = warp_id(), lane = lane_id(), b = blockIdx.y;
-  const int ch = blockIdx.x / cluster * kTile + 2 * lane, n = min(max(p.D - ch, 0), 2);
-  const bool tied = p.tied;
-  const T* x = static_cast<const T*>(p.x.ptr) + b * p.x.batch + ch;
-  const T* z = static_cast<const T*>(p.z.ptr) + b * p.z.batch + ch;
-  const T* d = static_cast<const T*>(p.dh.ptr) + (p.dh.ptr ? b * p.dh.batch + ch : 0);
-  const bool has_d = p.dh.ptr != nullptr;
-  T* ox = static_cast<T*>(p.dx.ptr) + b * p.dx.batch + ch;
-  T* oz = static_cast<T*>(p.dz.ptr) + b * p.dz.batch + ch;
+  const int c0 = blockIdx.x / cluster * 64, ch = c0 + 2 * lane, n = min(max(p.D - ch, 0), 2);
+  uint8_t* mine = dynamic + w * 2 * 3 * kRowsBytes;
   const uint8_t* m = p.mask ? p.mask + static_cast<size_t>(b) * p.L : nullptr;
   const size_t state_at = static_cast<size_t>(b) * p.D + ch;
-  const int nsave = (p.L + kScanSave - 1) / kScanSave;
-  const int steps = (nsave + cluster - 1) / cluster;
+  const int chunks = (p.L + R - 1) / R, steps = (chunks + cluster * kWarps - 1) / (cluster * kWarps);
+  const float* saved = p.saved + static_cast<size_t>(b) * chunks * p.D + ch;
 
-  Raw xr[R], zr[R], dr[R];
-  uint64_t sr;
-  uint32_t bits;
-  auto load = [&](int k) {  // block of rows k, or none when k < 0
-    const int t0 = k * kScanSave + w * R;
-    bits = k < 0 ? 0u : valid_rows<R>(m, t0, p.L);
-    sr = k < 0 ? 0ull : load_state<PAIRED>(p.saved + (static_cast<size_t>(b) * nsave + k) * p.D + ch, n);
-    const T* xp = x + static_cast<long long>(t0) * p.x.row;
-    const T* zp = z + static_cast<long long>(t0) * p.z.row;
-    const T* dp = d + static_cast<long long>(t0) * p.dh.row;
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int q = bits >> r & 1 ? n : 0;
-      xr[r] = load_pair<T, PAIRED>(xp + r * p.x.row, q, P::zero());
-      zr[r] = load_pair<T, PAIRED>(zp + r * p.z.row, q, P::inf());
-      dr[r] = load_pair<T, PAIRED>(dp + r * p.dh.row, has_d ? q : 0, P::zero());
+  uint32_t coming = 0;
+  uint64_t state = 0ull;
+  auto start_step = [&](int step) {
+    const int c = chunks - 1 - ((step * cluster + rank) * kWarps + w);
+    coming = 0;
+    if (step < steps) {
+      if (c >= 0) coming = valid_rows<R>(m, c * R, p.L);
+      uint8_t* to = mine + (step & 1) * 3 * kRowsBytes;
+      const int t0 = max(c, 0) * R;
+      fetch<T, VEC>(to, p.x, b, t0, c0, p.D, coming, P::zero());
+      fetch<T, VEC>(to + kRowsBytes, p.z, b, t0, c0, p.D, coming, P::inf());
+      fetch<T, VEC>(to + 2 * kRowsBytes, p.dh, b, t0, c0, p.D, p.dh.ptr ? coming : 0u, P::zero());
+      state = c >= 0 ? load_state<VEC>(saved + static_cast<size_t>(c) * p.D, n) : 0ull;
     }
+    copies_commit();
   };
 
-  uint64_t carry = p.dlast ? load_state<PAIRED>(p.dlast + state_at, n) : 0ull;
-  load(nsave - 1 - rank);
+  start_step(0);
+  uint64_t carry = p.dlast ? load_state<VEC>(p.dlast + state_at, n) : 0ull;
   if (cluster > 1) cluster_sync();
   for (int step = 0; step < steps; ++step) {
-    const int k = nsave - 1 - step * cluster - rank, t0 = k * kScanSave + w * R;
-    uint64_t nc[R], slope[R], before[R], prod = f2_both(1.f), h = 0ull, g = 0ull;
-    Raw xs[R], ds[R];
-    const uint32_t now = bits;
-    uint64_t state = sr;
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      xs[r] = xr[r];
-      ds[r] = dr[r];
-      nc[r] = neg_decay<T, TAU1, true>(P::f32(zr[r]), p.inv_tau, slope[r]);
-    }
-    if (step + 1 < steps) load(k - cluster);
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      h = advance(h, nc[r], P::f32(xs[r]), tied);
-      prod = f2_fma(nc[r], prod, prod);
-    }
+    const int c = chunks - 1 - ((step * cluster + rank) * kWarps + w);
+    const uint32_t now = coming;
+    const uint64_t h = state;
+    __syncwarp();
+    start_step(step + 1);
+    copies_wait<1>();
+    __syncwarp();
+    uint8_t* rows = mine + (step & 1) * 3 * kRowsBytes;
+    Raw* xs = reinterpret_cast<Raw*>(rows) + lane;
+    Raw* zs = xs + kRowsBytes / sizeof(Raw);
+    const Raw* ds = zs + kRowsBytes / sizeof(Raw);
+    uint64_t nc[R], q[R];
+    row_factors<T, TAU1, TIED>(xs, zs, h, p.gate, nc, q);
+    Join join{f2_both(1.f), 0ull};
 #pragma unroll
     for (int r = R - 1; r >= 0; --r) {
-      g = f2_add(g, P::f32(ds[r]));
-      g = f2_fma(nc[r], g, g);
+      join.v = f2_add(join.v, P::f32(ds[r * 32]));
+      join.v = f2_fma(nc[r], join.v, join.v);
+      join.p = f2_fma(nc[r], join.p, join.p);
     }
-    warps[w][lane] = Join{prod, h};
-    grads[w][lane] = g;
+    Join(*wj)[32] = warps[step & 1];
+    wj[w][lane] = join;
     __syncthreads();
-#pragma unroll
-    for (int j = 0; j < W - 1; ++j) {
-      const Join q = warps[j][lane];
-      if (j < w) state = f2_fma(q.p, state, q.v);
-    }
-    Join after{f2_both(1.f), 0ull}, all{f2_both(1.f), 0ull};
-#pragma unroll
-    for (int j = W - 1; j >= 0; --j) {
-      if (j == w) after = all;
-      const uint64_t q = warps[j][lane].p;
-      all.v = f2_fma(q, all.v, grads[j][lane]);
-      all.p = f2_mul(q, all.p);
-    }
     uint64_t in = carry;
-    if (cluster > 1) {
-      Join* slots = blocks[step & 1];
+    if (cluster == 1) {
+#pragma unroll
+      for (int j = 0; j < kWarps; ++j) {
+        if (j == w) in = carry;
+        const Join v = wj[j][lane];
+        carry = f2_fma(v.p, carry, v.v);
+      }
+    } else {
+      Join before{f2_both(1.f), 0ull}, all{f2_both(1.f), 0ull};
+#pragma unroll
+      for (int j = 0; j < kWarps; ++j) {
+        if (j == w) before = all;
+        const Join v = wj[j][lane];
+        all.v = f2_fma(v.p, all.v, v.v);
+        all.p = f2_mul(v.p, all.p);
+      }
+      Join* slots = reinterpret_cast<Join*>(dynamic + kBackRows) + (step & 1) * cluster * 32;
       send_join(slots, rank, cluster, all, w == 0);
       for (int j = 0; j < cluster; ++j) {
         if (j == rank) in = carry;
-        const Join q = slots[j * 32 + lane];
-        carry = f2_fma(q.p, carry, q.v);
+        const Join v = slots[j * 32 + lane];
+        carry = f2_fma(v.p, carry, v.v);
       }
-    } else {
-      carry = f2_fma(all.p, carry, all.v);
-      __syncthreads();
+      in = f2_fma(before.p, in, before.v);
     }
-    in = f2_fma(after.p, in, after.v);
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const uint64_t xv = P::f32(xs[r]);
-      before[r] = tied ? f2_add(state, f2_neg(xv)) : state;
-      state = advance(state, nc[r], xv, tied);
-    }
-    T* xp = ox + static_cast<long long>(t0) * p.dx.row;
-    T* zp = oz + static_cast<long long>(t0) * p.dz.row;
 #pragma unroll
     for (int r = R - 1; r >= 0; --r) {
-      g = f2_add(in, P::f32(ds[r]));
-      const uint64_t gz = f2_mul(f2_mul(g, before[r]), slope[r]), gx = tied ? f2_neg(f2_mul(nc[r], g)) : g;
+      const uint64_t g = f2_add(in, P::f32(ds[r * 32]));
       in = f2_fma(nc[r], g, g);
-      if (now >> r & 1) {
-        store_pair<T, PAIRED>(xp + r * p.dx.row, n, P::round(gx));
-        store_pair<T, PAIRED>(zp + r * p.dz.row, n, P::round(gz));
-      } else {
-        in = g;  // a padded row hands on what it got
-        if (k >= 0 && t0 + r < p.L) {
-          store_pair<T, PAIRED>(xp + r * p.dx.row, n, P::zero());
-          store_pair<T, PAIRED>(zp + r * p.dz.row, n, P::zero());
-        }
-      }
+      xs[r * 32] = P::round(input_grad<TIED>(nc[r], g));
+      zs[r * 32] = P::round(f2_mul(g, q[r]));
+    }
+    __syncwarp();
+    if (c >= 0) {
+      put<T, VEC>(rows, p.dx, b, c * R, c0, p.D, p.L, now);
+      put<T, VEC>(rows + kRowsBytes, p.dz, b, c * R, c0, p.D, p.L, now);
     }
   }
-  if (p.dh0 && rank == 0 && w == 0) store_state<PAIRED>(p.dh0 + state_at, n, carry);
+  if (p.dh0 && rank == 0 && w == 0) store_state<VEC>(p.dh0 + state_at, n, carry);
 }
 
 // ---------------------------------------------------------------- single tokens
-template <typename T, bool PAIRED, bool TAU1>
+template <typename T, bool VEC, bool TAU1, bool TIED>
 __global__ void __launch_bounds__(128) scan_step_kernel(const StepParams p) {
   using P = Pair<T>;
   const int ch = (blockIdx.x * 128 + threadIdx.x) * 2, n = min(max(p.D - ch, 0), 2), b = blockIdx.y;
@@ -465,39 +838,42 @@ __global__ void __launch_bounds__(128) scan_step_kernel(const StepParams p) {
   typename P::Raw out = P::zero();
   if (!p.mask || p.mask[b]) {
     float* s = p.state + static_cast<size_t>(b) * p.D + ch;
-    uint64_t unused;
-    const uint64_t z = P::f32(load_pair<T, PAIRED>(static_cast<const T*>(p.z) + b * p.z_row + ch, n, P::inf()));
-    const uint64_t x = P::f32(load_pair<T, PAIRED>(static_cast<const T*>(p.x) + b * p.x_row + ch, n, P::zero()));
-    const uint64_t h = advance(load_state<PAIRED>(s, n), neg_decay<T, TAU1, false>(z, p.inv_tau, unused), x, p.tied);
-    store_state<PAIRED>(s, n, h);
+    const uint64_t z = P::f32(load_pair<T, VEC>(static_cast<const T*>(p.z) + b * p.z_row + ch, n, P::inf()));
+    const uint64_t x = P::f32(load_pair<T, VEC>(static_cast<const T*>(p.x) + b * p.x_row + ch, n, P::zero()));
+    float far = 0.f;
+    const uint64_t zz[1] = {z};
+    uint64_t nc[1];
+    neg_decay<T, TAU1>(zz, p.gate, far, nc);
+    if (kExpansion<T, TAU1> && far > p.gate.far) nc[0] = neg_decay_far(z, p.gate);
+    const uint64_t h = advance<TIED>(load_state<VEC>(s, n), nc[0], x);
+    store_state<VEC>(s, n, h);
     out = P::round(h);
   }
-  store_pair<T, PAIRED>(static_cast<T*>(p.h) + b * p.h_row + ch, n, out);
+  store_pair<T, VEC>(static_cast<T*>(p.h) + b * p.h_row + ch, n, out);
 }
 
 // ---------------------------------------------------------------- launches
-// f(element type, PAIRED, TAU1) with the values as compile-time constants
+// f(element type, VEC, TAU1, TIED) with the values as compile-time constants
 template <typename F>
-void by_kind(int dtype, bool paired, bool tau1, F&& f) {
-  auto by_tau = [&](auto t, auto pr) {
-    if (tau1) f(t, pr, std::true_type{});
-    else f(t, pr, std::false_type{});
+void by_kind(int dtype, bool vec, bool tau1, bool tied, F&& f) {
+  auto pick = [](bool v, auto&& g) {
+    if (v) g(std::true_type{});
+    else g(std::false_type{});
   };
-  auto by_pair = [&](auto t) {
-    if (paired) by_tau(t, std::true_type{});
-    else by_tau(t, std::false_type{});
+  auto by_type = [&](auto t) {
+    pick(vec, [&](auto v) { pick(tau1, [&](auto u) { pick(tied, [&](auto i) { f(t, v, u, i); }); }); });
   };
-  if (dtype == kBF16) by_pair(__nv_bfloat16{});
-  else if (dtype == kF16) by_pair(__half{});
-  else by_pair(float{});
+  if (dtype == kBF16) by_type(__nv_bfloat16{});
+  else if (dtype == kF16) by_type(__half{});
+  else by_type(float{});
 }
 
-// Whether pairs of channels are aligned in every row of r.
-bool paired_rows(const Rows& r, int dtype) {
-  const uintptr_t pair = dtype == kF32 ? 8 : 4;
-  return !r.ptr || (reinterpret_cast<uintptr_t>(r.ptr) % pair == 0 && r.batch % 2 == 0 && r.row % 2 == 0);
+// Whether runs of `run` channels from a multiple of `run` on are aligned in every row of r.
+bool aligned_rows(const Rows& r, int run, int dtype) {
+  const uintptr_t bytes = run * (dtype == kF32 ? 4 : 2);
+  return !r.ptr || (reinterpret_cast<uintptr_t>(r.ptr) % bytes == 0 && r.batch % run == 0 && r.row % run == 0);
 }
-bool paired_state(const float* s) { return reinterpret_cast<uintptr_t>(s) % 8 == 0; }
+bool aligned_state(const float* s) { return reinterpret_cast<uintptr_t>(s) % 8 == 0; }
 
 int multiprocessors() {
   int dev = 0, n = 148;
@@ -505,25 +881,39 @@ int multiprocessors() {
   return n;
 }
 
-// Blocks per channel tile: the smallest cluster among those that fill the GPU best (blocks
-// in whole waves of `resident`), and no more blocks than the rows need.
-int pick_cluster(int tiles, int L, int rows, int resident) {
-  int best = 1;
-  double best_fill = 0;
-  for (int c = 1; c <= kMaxCluster; c *= 2) {
-    if (c > 1 && static_cast<long long>(c / 2) * rows >= L) break;
-    const double blocks = static_cast<double>(tiles) * c, waves = std::ceil(blocks / resident);
-    const double fill = blocks / (waves * resident);
-    if (fill > best_fill * 1.02) best = c, best_fill = fill;
-  }
-  return best;
+// Whether one chain per channel tile and sequence is the form to take, or rows are split.
+bool one_chain(long long tiles, int L) {
+  if (const char* e = getenv("SCAN_CHAIN")) return atoi(e);  // TEMP
+  return tiles >= 96 || L <= 1024;
+}
+
+// Blocks per channel tile where rows are split: enough to give every SM one.
+int pick_cluster(long long tiles, int L, int rows) {
+  int c = 1;
+  while (c < kMaxCluster && tiles * c < multiprocessors() && static_cast<long long>(c) * rows < L) c *= 2;
+  return c;
+}
+
+// (e^{-s} - 1) / s on [0, 1/2]: a Chebyshev expansion cut off at degree 4 (relative error
+// 6e-8), with the powers of 1 / tau in its coefficients.
+DecayParams decay_params(float inv_tau) {
+  const double k[5] = {-0.99999994, 0.4999924, -0.166547343, 0.0409987494, -0.0067685456};
+  DecayParams g;
+  g.inv_tau = inv_tau;
+  g.far = 0.5f / inv_tau;
+  double power = inv_tau;
+  for (int i = 0; i < 5; ++i, power *= inv_tau) g.expm1[i] = make_float2(static_cast<float>(k[i] * power), static_cast<float>(k[i] * power));
+  return g;
 }
 
 template <typename K>
-cudaError_t launch(K kernel, const ScanParams& p, int threads, cudaStream_t st) {
+cudaError_t launch(K kernel, const ScanParams& p, int threads, int shared, cudaStream_t st) {
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, shared);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((p.D + kTile - 1) / kTile * p.cluster, p.B);
+  cfg.gridDim = dim3((p.D + 63) / 64 * p.cluster, p.B);
   cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = shared;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -536,42 +926,63 @@ cudaError_t launch(K kernel, const ScanParams& p, int threads, cudaStream_t st) 
 
 }  // namespace
 
+int scan_saved_rows(int dtype) { return dtype == kF32 ? kRowsOf<float> : kRowsOf<__half>; }
+
 cudaError_t launch_scan_forward(const ScanParams& params, cudaStream_t st) {
   ScanParams p = params;
-  const bool paired = p.D % 2 == 0 && paired_rows(p.x, p.dtype) && paired_rows(p.z, p.dtype) && paired_rows(p.h, p.dtype) &&
-                      paired_state(p.h0) && paired_state(p.last) && paired_state(p.saved);
+  p.gate = decay_params(p.inv_tau);
+  const int run = p.dtype == kF32 ? 4 : 8;
+  const bool vec = p.D % run == 0 && aligned_rows(p.x, run, p.dtype) && aligned_rows(p.z, run, p.dtype) &&
+                   aligned_rows(p.h, run, p.dtype) && aligned_state(p.h0) && aligned_state(p.last) && aligned_state(p.saved);
+  const long long tiles = (p.D + 63LL) / 64 * p.B;
   cudaError_t e = cudaSuccess;
-  by_kind(p.dtype, paired, p.inv_tau == 1.f, [&](auto t, auto pr, auto tau1) {
+  by_kind(p.dtype, vec, p.inv_tau == 1.f, p.tied, [&](auto t, auto v, auto u, auto i) {
     using T = decltype(t);
-    constexpr int W = 8, R = sizeof(T) == 4 ? 8 : 16;
-    p.cluster = pick_cluster((p.D + kTile - 1) / kTile * p.B, p.L, W * R, 2 * multiprocessors());
-    e = launch(scan_forward_kernel<T, W, R, decltype(pr)::value, decltype(tau1)::value>, p, W * 32, st);
+    constexpr bool V = decltype(v)::value, U = decltype(u)::value, I = decltype(i)::value;
+    if (one_chain(tiles, p.L)) {
+      p.cluster = 1;
+      e = launch(scan_chain_kernel<T, V, U, I>, p, kChainThreads, kChainShared, st);
+    } else {
+      p.cluster = pick_cluster(tiles, p.L, kWarps * kRowsOf<T>);
+      e = launch(scan_forward_kernel<T, V, U, I>, p, kWarps * 32, kForwardRows + (p.cluster > 1 ? p.cluster * kSlots : 0), st);
+    }
   });
   return e;
 }
 
 cudaError_t launch_scan_backward(const ScanParams& params, cudaStream_t st) {
   ScanParams p = params;
-  const bool paired = p.D % 2 == 0 && paired_rows(p.x, p.dtype) && paired_rows(p.z, p.dtype) && paired_rows(p.dh, p.dtype) &&
-                      paired_rows(p.dx, p.dtype) && paired_rows(p.dz, p.dtype) && paired_state(p.saved) &&
-                      paired_state(p.dlast) && paired_state(p.dh0);
+  p.gate = decay_params(p.inv_tau);
+  const int run = p.dtype == kF32 ? 4 : 8;
+  const bool vec = p.D % run == 0 && aligned_rows(p.x, run, p.dtype) && aligned_rows(p.z, run, p.dtype) &&
+                   aligned_rows(p.dh, run, p.dtype) && aligned_rows(p.dx, run, p.dtype) &&
+                   aligned_rows(p.dz, run, p.dtype) && aligned_state(p.saved) && aligned_state(p.dlast) &&
+                   aligned_state(p.dh0);
+  const long long tiles = (p.D + 63LL) / 64 * p.B;
   cudaError_t e = cudaSuccess;
-  by_kind(p.dtype, paired, p.inv_tau == 1.f, [&](auto t, auto pr, auto tau1) {
+  by_kind(p.dtype, vec, p.inv_tau == 1.f, p.tied, [&](auto t, auto v, auto u, auto i) {
     using T = decltype(t);
-    constexpr int W = sizeof(T) == 4 ? 16 : 8, R = kScanSave / W;
-    p.cluster = pick_cluster((p.D + kTile - 1) / kTile * p.B, p.L, W * R, (W == 8 ? 2 : 1) * multiprocessors());
-    e = launch(scan_backward_kernel<T, W, R, decltype(pr)::value, decltype(tau1)::value>, p, W * 32, st);
+    constexpr bool V = decltype(v)::value, U = decltype(u)::value, I = decltype(i)::value;
+    if (one_chain(tiles, p.L)) {
+      p.cluster = 1;
+      e = launch(scan_chain_backward_kernel<T, V, U, I>, p, kWorkers * 32 + 32, kBackShared, st);
+    } else {
+      p.cluster = pick_cluster(tiles, p.L, kWarps * kRowsOf<T>);
+      e = launch(scan_backward_kernel<T, V, U, I>, p, kWarps * 32, kBackRows + (p.cluster > 1 ? p.cluster * kSlots : 0), st);
+    }
   });
   return e;
 }
 
-cudaError_t launch_scan_step(const StepParams& p, cudaStream_t st) {
+cudaError_t launch_scan_step(const StepParams& params, cudaStream_t st) {
+  StepParams p = params;
+  p.gate = decay_params(p.inv_tau);
   const Rows rows[3] = {{const_cast<void*>(p.x), p.x_row, 0}, {const_cast<void*>(p.z), p.z_row, 0}, {p.h, p.h_row, 0}};
-  bool paired = p.D % 2 == 0 && paired_state(p.state);
-  for (const Rows& r : rows) paired = paired && paired_rows(r, p.dtype);
+  bool vec = p.D % 2 == 0 && aligned_state(p.state);
+  for (const Rows& r : rows) vec = vec && aligned_rows(r, 2, p.dtype);
   const dim3 grid((p.D + 255) / 256, p.B);
-  by_kind(p.dtype, paired, p.inv_tau == 1.f, [&](auto t, auto pr, auto tau1) {
-    scan_step_kernel<decltype(t), decltype(pr)::value, decltype(tau1)::value><<<grid, 128, 0, st>>>(p);
+  by_kind(p.dtype, vec, p.inv_tau == 1.f, p.tied, [&](auto t, auto v, auto tau1, auto tied) {
+    scan_step_kernel<decltype(t), decltype(v)::value, decltype(tau1)::value, decltype(tied)::value><<<grid, 128, 0, st>>>(p);
   });
   return cudaGetLastError();
 }

@@ -92,15 +92,16 @@ int check_scan(const msgla_scan_config* c, int B, int L) {
   if (c->dtype < MSGLA_BF16 || c->dtype > MSGLA_F32) return set_error(MSGLA_ERR_INVALID_ARG, "dtype=%d", c->dtype);
   if (c->D < 1 || c->D > 1 << 24) return set_error(MSGLA_ERR_INVALID_ARG, "D=%d outside [1, 2^24]", c->D);
   if (c->tied != 0 && c->tied != 1) return set_error(MSGLA_ERR_INVALID_ARG, "tied=%d must be 0 or 1", c->tied);
-  if (!(c->gate_normalizer > 0.f) || !std::isfinite(c->gate_normalizer) || !std::isfinite(1.f / c->gate_normalizer))
-    return set_error(MSGLA_ERR_INVALID_ARG, "gate_normalizer must be positive and finite, and so its reciprocal");
+  if (!(c->gate_normalizer >= 0x1p-10f && c->gate_normalizer <= 0x1p20f))
+    return set_error(MSGLA_ERR_INVALID_ARG, "gate_normalizer=%g outside [2^-10, 2^20]", c->gate_normalizer);
   if (B < 0 || B > 65535) return set_error(MSGLA_ERR_INVALID_ARG, "B=%d outside [0, 65535]", B);
   if (L < 0 || L > 1 << 30) return set_error(MSGLA_ERR_INVALID_ARG, "L=%d outside [0, 2^30]", L);
   return MSGLA_OK;
 }
 
 size_t saved_bytes(const msgla_scan_config* c, int B, int L) {
-  return static_cast<size_t>(B) * ((static_cast<size_t>(L) + kScanSave - 1) / kScanSave) * c->D * 4;
+  const int rows = scan_saved_rows(c->dtype);
+  return static_cast<size_t>(B) * ((static_cast<size_t>(L) + rows - 1) / rows) * c->D * 4;
 }
 
 ScanParams scan_params(const msgla_scan_config* c, int B, int L, const void* M) {

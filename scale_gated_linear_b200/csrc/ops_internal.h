@@ -20,17 +20,25 @@ struct Rows {
 };
 
 // ---------------------------------------------------------------- gated recurrence
-constexpr int kScanSave = 64;  // rows between two saved states
+int scan_saved_rows(int dtype);  // rows between two saved states
+
+// The gate as its kernels use it (set by the launches): 1 / tau, tau / 2, and the
+// polynomial of (e^{-S / tau} - 1) / S, both halves of every packed operand.
+struct DecayParams {
+  float inv_tau, far;
+  float2 expm1[5];
+};
 
 struct ScanParams {
   int dtype, B, L, D, tied;
   int cluster;          // blocks per channel tile (set by the launches)
   float inv_tau;
+  DecayParams gate;
   Rows x, z, h, dh, dx, dz;
   const uint8_t* mask;  // [B, L] or null
   const float* h0;      // [B, D] or null (zeros)
   float* last;          // [B, D]
-  float* saved;         // [B, ceil(L / kScanSave), D] states before rows 0, kScanSave, ...; or null
+  float* saved;         // [B, ceil(L / rows), D] states before rows 0, rows, 2 rows, ...; or null
   const float* dlast;   // [B, D] or null
   float* dh0;           // [B, D] or null
 };
@@ -40,6 +48,7 @@ cudaError_t launch_scan_backward(const ScanParams& p, cudaStream_t st);
 struct StepParams {
   int dtype, B, D, tied;
   float inv_tau;
+  DecayParams gate;
   const void *x, *z;
   void* h;
   long long x_row, z_row, h_row;

@@ -168,7 +168,8 @@ def _scan_forward(x, gate, mask, initial_state, gate_normalizer, tied, save, out
     else:
         _check_out(out, x)
     last = on.empty((B, D), torch.float32, x.device)
-    states = on.empty((B, (L + 63) // 64, D), torch.float32, x.device) if save else None
+    rows = 8 if x.dtype == torch.float32 else 16
+    states = on.empty((B, (L + rows - 1) // rows, D), torch.float32, x.device) if save else None
     _lib.check(_lib.load().msgla_scan_forward(cfg, B, L, _rows3("x", x), _rows3("gate", gate), _ptr(mask),
                                               _ptr(initial_state), _rows3("out", out), last.data_ptr(), _ptr(states),
                                               on.handle))

@@ -43,10 +43,9 @@ def test_scan_rejects_bad_config(kw):
 
 def test_scan_sizes():
     lib, n = _lib.load(), ctypes.c_size_t()
-    for L, want in ((0, 0), (1, 1), (64, 1), (65, 2), (1 << 20, 1 << 14)):
-        assert lib.msgla_scan_saved_size(scan_cfg(), 3, L, ctypes.byref(n)) == 0 and n.value == 3 * want * 8 * 4
-    assert lib.msgla_scan_saved_size(scan_cfg(D=1 << 20), 65535, 1 << 30, ctypes.byref(n)) == 0
-    assert n.value == 65535 * (1 << 24) * (1 << 20) * 4 % 2 ** 64
+    for dtype, rows in ((0, 16), (1, 16), (2, 8)):
+        for L, want in ((0, 0), (1, 1), (rows, 1), (rows + 1, 2), (1 << 20, (1 << 20) // rows)):
+            assert lib.msgla_scan_saved_size(scan_cfg(dtype=dtype), 3, L, ctypes.byref(n)) == 0 and n.value == 3 * want * 8 * 4
     for B, L in ((-1, 1), (65536, 1), (1, -1), (1, (1 << 30) + 1)):
         assert lib.msgla_scan_saved_size(scan_cfg(), B, L, ctypes.byref(n)) == -1
     assert lib.msgla_scan_saved_size(scan_cfg(), 1, 1, None) == -1
