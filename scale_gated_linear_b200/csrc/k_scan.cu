@@ -326,64 +326,80 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Starts a warp's copy of rows t0 .. t0 + R - 1 of channels c0 .. c0 + 63 to `to`; rows whose bit
-// is not set and channels past D become `none`. VEC: 16-byte copies (rows aligned to 16
-// bytes and D a whole number of them); else the lanes load and store their pairs at once.
-template <typename T, bool VEC, int R = kRowsOf<T>>
-__device__ __forceinline__ void fetch(uint8_t* to, const Rows& r, int b, int t0, int c0, int D, uint32_t bits,
+// Where a lane's part of a warp's rows stands: 16 bytes of every kEach-th row with VEC (rows
+// aligned to 16 bytes, D a whole number of them), else the lane's pair of every row.
+template <typename T, bool VEC>
+struct Lane {
+  static constexpr int kRow = 64 * sizeof(T), kEach = VEC ? 512 / kRow : 1;
+  T* at;            // in the row given to go_to
+  long long row;
+  int first, n;     // its first row, its channels inside D
+  __device__ __forceinline__ Lane(const Rows& r, int b, int c0, int D) {
+    const int c = VEC ? lane_id() * 16 % kRow / static_cast<int>(sizeof(T)) : 2 * lane_id();
+    first = VEC ? lane_id() * 16 / kRow : 0;
+    n = min(max(D - c0 - c, 0), VEC ? 16 / static_cast<int>(sizeof(T)) : 2);
+    row = r.row;
+    at = static_cast<T*>(r.ptr) + b * r.batch + first * r.row + c0 + c;
+  }
+  __device__ __forceinline__ void move(long long rows) { at += rows * row; }
+};
+
+// Starts a warp's copy of R rows to `to`; rows whose bit is not set and channels past D
+// become `none`. full: every row is valid and every channel inside D. Without VEC the lanes load
+// and store their pairs at once.
+template <typename T, bool VEC>
+__device__ __forceinline__ void fetch(uint8_t* to, const Lane<T, VEC>& l, bool full, uint32_t bits,
                                       typename Pair<T>::Raw none) {
-  constexpr int kRow = 64 * sizeof(T), kEach = 512 / kRow;
+  constexpr int R = kRowsOf<T>, kEach = Lane<T, VEC>::kEach;
+  const T* from = l.at;
   const int lane = lane_id();
-  const T* base = static_cast<const T*>(r.ptr) + b * r.batch + static_cast<long long>(t0) * r.row + c0;
   if constexpr (VEC) {
-    const int row = lane * 16 / kRow, col = lane * 16 % kRow;
-    const bool inside = c0 + col / static_cast<int>(sizeof(T)) < D;
-    const T* from = base + row * r.row + col / sizeof(T);
-    const uint32_t at = smem_u32(to) + lane * 16;
-    bits >>= row;
+    const uint32_t at = smem_u32(to) + lane * 16, v = static_cast<uint32_t>(none);  // a 64-bit pair's halves are alike
+    if (full) {
 #pragma unroll
-    for (int i = 0; i < R / kEach; ++i, from += kEach * r.row) {
-      if (inside && (bits >> i * kEach & 1)) {
-        copy16(at + i * 512, from);
-      } else {
-        uint32_t v = static_cast<uint32_t>(none);  // the halves of a 64-bit pair are alike
-        st_shared_v4(at + i * 512, v, v, v, v);
+      for (int i = 0; i < R / kEach; ++i, from += kEach * l.row) copy16(at + i * 512, from);
+    } else {
+      bits >>= l.first;
+#pragma unroll
+      for (int i = 0; i < R / kEach; ++i, from += kEach * l.row) {
+        if (l.n && (bits >> i * kEach & 1)) copy16(at + i * 512, from);
+        else st_shared_v4(at + i * 512, v, v, v, v);
       }
     }
   } else {
-    const int n = min(max(D - c0 - 2 * lane, 0), 2);
 #pragma unroll 4
-    for (int i = 0; i < R; ++i)
-      reinterpret_cast<typename Pair<T>::Raw*>(to + i * kRow)[lane] =
-          load_pair<T, false>(base + i * r.row + 2 * lane, bits >> i & 1 ? n : 0, none);
+    for (int i = 0; i < R; ++i, from += l.row)
+      reinterpret_cast<typename Pair<T>::Raw*>(to + i * Lane<T, VEC>::kRow)[lane] =
+          load_pair<T, false>(from, bits >> i & 1 ? l.n : 0, none);
   }
 }
 
-// Stores a warp's rows t0 .. from shared memory; rows whose bit is not set as zeros.
-template <typename T, bool VEC, int R = kRowsOf<T>>
-__device__ __forceinline__ void put(const uint8_t* from, const Rows& r, int b, int t0, int c0, int D, int L, uint32_t bits) {
-  constexpr int kRow = 64 * sizeof(T), kEach = 512 / kRow;
+// Stores the first `rows` (1 .. R) of a warp's rows from shared memory; those whose bit is
+// not set as zeros.
+template <typename T, bool VEC>
+__device__ __forceinline__ void put(const uint8_t* from, const Lane<T, VEC>& l, bool full, int rows, uint32_t bits) {
+  constexpr int R = kRowsOf<T>, kEach = Lane<T, VEC>::kEach;
   const int lane = lane_id();
-  T* base = static_cast<T*>(r.ptr) + b * r.batch + static_cast<long long>(t0) * r.row + c0;
+  T* to = l.at;
   if constexpr (VEC) {
-    const int row = lane * 16 / kRow, col = lane * 16 % kRow;
-    const int last = c0 + col / static_cast<int>(sizeof(T)) < D ? L - t0 - row : 0;
-    T* to = base + row * r.row + col / sizeof(T);
-    bits >>= row;
+    const uint4* v = reinterpret_cast<const uint4*>(from) + lane;
+    if (full) {
 #pragma unroll
-    for (int i = 0; i < R / kEach; ++i, to += kEach * r.row) {
-      uint4 v = reinterpret_cast<const uint4*>(from)[i * 32 + lane];
-      if (!(bits >> i * kEach & 1)) v = make_uint4(0, 0, 0, 0);
-      if (i * kEach < last) *reinterpret_cast<uint4*>(to) = v;
+      for (int i = 0; i < R / kEach; ++i, to += kEach * l.row) *reinterpret_cast<uint4*>(to) = v[i * 32];
+    } else {
+      bits >>= l.first;
+      rows -= l.first;
+#pragma unroll
+      for (int i = 0; i < R / kEach; ++i, to += kEach * l.row)
+        if (l.n && i * kEach < rows) *reinterpret_cast<uint4*>(to) = bits >> i * kEach & 1 ? v[i * 32] : make_uint4(0, 0, 0, 0);
     }
   } else {
     using Raw = typename Pair<T>::Raw;
-    const int n = min(max(D - c0 - 2 * lane, 0), 2);
 #pragma unroll 4
-    for (int i = 0; i < R; ++i)
-      if (t0 + i < L)
-        store_pair<T, false>(base + i * r.row + 2 * lane, n,
-                             bits >> i & 1 ? reinterpret_cast<const Raw*>(from + i * kRow)[lane] : Pair<T>::zero());
+    for (int i = 0; i < R; ++i, to += l.row)
+      if (i < rows)
+        store_pair<T, false>(to, l.n, bits >> i & 1 ? reinterpret_cast<const Raw*>(from + i * Lane<T, VEC>::kRow)[lane]
+                                                    : Pair<T>::zero());
   }
 }
 
@@ -409,13 +425,18 @@ __global__ void __launch_bounds__(kWarps * 32, 3) scan_forward_kernel(const Scan
   const int chunks = (p.L + R - 1) / R, steps = (p.L + cluster * kRows - 1) / (cluster * kRows);
 
   uint32_t coming;  // valid rows on their way
+  const bool inside = c0 + 64 <= p.D;
+  Lane<T, VEC> lx(p.x, b, c0, p.D), lz(p.z, b, c0, p.D), lo(p.h, b, c0, p.D);
+  const int first = (rank * kWarps + w) * R;
+  lx.move(first), lz.move(first), lo.move(first);
   auto start_step = [&](int step) {
     if (step < steps) {
-      const int t0 = ((step * cluster + rank) * kWarps + w) * R;
       uint8_t* to = mine + step % kStages * 2 * kRowsBytes;
-      coming = valid_rows<R>(m, t0, p.L);
-      fetch<T, VEC>(to, p.x, b, t0, c0, p.D, coming, P::zero());
-      fetch<T, VEC>(to + kRowsBytes, p.z, b, t0, c0, p.D, coming, P::inf());
+      coming = valid_rows<R>(m, first + step * cluster * kRows, p.L);
+      const bool full = inside && coming == (1u << R) - 1u;
+      fetch<T, VEC>(to, lx, full, coming, P::zero());
+      fetch<T, VEC>(to + kRowsBytes, lz, full, coming, P::inf());
+      lx.move(cluster * kRows), lz.move(cluster * kRows);
     }
     copies_commit();
   };
@@ -477,107 +498,98 @@ __global__ void __launch_bounds__(kWarps * 32, 3) scan_forward_kernel(const Scan
       xs[r * 32] = P::round(h);
     }
     __syncwarp();
-    put<T, VEC>(rows, p.h, b, t0, c0, p.D, p.L, now);
+    if (t0 < p.L) put<T, VEC>(rows, lo, inside && now == (1u << R) - 1u, min(p.L - t0, R), now);
+    lo.move(cluster * kRows);
   }
   if (rank == 0 && w == 0) store_state<VEC>(p.last + state_at, n, carry);
 }
 
-// ---------------------------------------------------------------- forward, one chain per tile
-// Groups of two warps load chunks and turn their logits into -c, one warp walks through the
-// chunks in order: h takes the place of x, and the group stores it. Named barriers of
-// the group's and the chain's threads hand a chunk over and back.
-constexpr int kGroups = 7, kGroupWarps = 2;
-constexpr int kMeeting = 32 * kGroupWarps + 32;
-constexpr int kChainThreads = kGroups * kGroupWarps * 32 + 32;
-__device__ __forceinline__ void meet(int id) { asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(kMeeting) : "memory"); }
-__device__ __forceinline__ void leave(int id) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "n"(kMeeting) : "memory"); }
+// ---------------------------------------------------------------- forward, one block per tile
+// The block's warps take the chunks of R rows in turn, each on its own: copies, gate, the
+// chunk's decay product and local end state. Only the true state goes from warp to warp in
+// the chunks' order, a relay with one named barrier a warp: a hop is one product and sum, and
+// the rows of a chunk follow from the state before it while the next warps go on.
+__device__ __forceinline__ void relay_wait(int warp) { asm volatile("bar.sync %0, 64;" ::"r"(1 + warp) : "memory"); }
+__device__ __forceinline__ void relay_pass(int warp) { asm volatile("bar.arrive %0, 64;" ::"r"(1 + warp) : "memory"); }
 
-constexpr int kRing = 3;  // chunks of a group in shared memory: one used, two on their way
-constexpr int kNcBytes = 2 * kRowsBytes;  // -c of a chunk as f32 (f32 tensors use half of it)
-constexpr int kChainGroup = kRing * 2 * kRowsBytes + kNcBytes;
-constexpr int kChainShared = kGroups * kChainGroup;
+constexpr int kRelay = 12;  // warps of a block
+constexpr int kRelayShared = kRelay * 2 * 2 * kRowsBytes;
 
 template <typename T, bool VEC, bool TAU1, bool TIED>
-__global__ void __launch_bounds__(kChainThreads, 2) scan_chain_kernel(const ScanParams p) {
+__global__ void __launch_bounds__(kRelay * 32, 2) scan_relay_kernel(const ScanParams p) {
   using P = Pair<T>;
   using Raw = typename P::Raw;
-  constexpr int R = kRowsOf<T>, RW = R / kGroupWarps, kRowsHere = RW * 64 * sizeof(T);
+  constexpr int R = kRowsOf<T>;
+  constexpr uint32_t kFull = (1u << R) - 1u;
   extern __shared__ __align__(128) uint8_t dynamic[];
+  __shared__ uint64_t baton[kRelay][32];
   const int w = warp_id(), lane = lane_id(), b = blockIdx.y, c0 = blockIdx.x * 64;
+  const int ch = c0 + 2 * lane, n = min(max(p.D - ch, 0), 2);
   const int chunks = (p.L + R - 1) / R;
-  if (w < kGroups * kGroupWarps) {
-    const int g = w / kGroupWarps, r0 = w % kGroupWarps * RW;  // this warp's rows of a chunk
-    uint8_t* mine = dynamic + g * kChainGroup + w % kGroupWarps * kRowsHere;
-    uint64_t* ncs = reinterpret_cast<uint64_t*>(dynamic + g * kChainGroup + kRing * 2 * kRowsBytes) + r0 * 32 + lane;
-    const uint8_t* m = p.mask ? p.mask + static_cast<size_t>(b) * p.L : nullptr;
-    auto start = [&](int c, int slot) {
-      uint32_t bits = 0;
-      if (c < chunks) {
-        bits = valid_rows<RW>(m, c * R + r0, p.L);
-        uint8_t* to = mine + slot * 2 * kRowsBytes;
-        fetch<T, VEC, RW>(to, p.x, b, c * R + r0, c0, p.D, bits, P::zero());
-        fetch<T, VEC, RW>(to + kRowsBytes, p.z, b, c * R + r0, c0, p.D, bits, P::inf());
-      }
-      copies_commit();
-      return bits;
-    };
-    uint32_t before = 0, now = start(g, 0), next = start(g + kGroups, 1);
-    int slot = 0;
-    for (int c = g; c < chunks + kGroups; c += kGroups) {
-      const int last = slot == 0 ? kRing - 1 : slot - 1;
-      if (c >= kGroups) meet(8 + g);  // the chain has been through the chunk before
-      if (c < chunks) {
-        copies_wait<1>();
-        __syncwarp();
-        const Raw* zs = reinterpret_cast<const Raw*>(mine + (slot * 2 + 1) * kRowsBytes) + lane;
-        uint64_t nc[RW];
-        row_decays<T, TAU1>(zs, p.gate, nc);
-#pragma unroll
-        for (int r = 0; r < RW; ++r) ncs[r * 32] = nc[r];
-        leave(1 + g);
-      }
-      if (c >= kGroups)
-        put<T, VEC, RW>(mine + last * 2 * kRowsBytes, p.h, b, (c - kGroups) * R + r0, c0, p.D, p.L, before);
-      __syncwarp();
-      before = now;
-      now = next;
-      next = start(c + 2 * kGroups, last);
-      slot = slot + 1 == kRing ? 0 : slot + 1;
+  const bool inside = c0 + 64 <= p.D;
+  const size_t state_at = static_cast<size_t>(b) * p.D + ch;
+  const uint8_t* m = p.mask ? p.mask + static_cast<size_t>(b) * p.L : nullptr;
+  uint8_t* mine = dynamic + w * 4 * kRowsBytes;
+  float* saved = p.saved ? p.saved + (static_cast<size_t>(b) * chunks + w) * p.D + ch : nullptr;
+  Lane<T, VEC> lx(p.x, b, c0, p.D), lz(p.z, b, c0, p.D), lo(p.h, b, c0, p.D);
+  lx.move(w * R), lz.move(w * R), lo.move(w * R);
+  auto start = [&](int c, int slot) {
+    uint32_t bits = 0;
+    if (c < chunks) {
+      uint8_t* to = mine + slot * 2 * kRowsBytes;
+      bits = !m && (c + 1) * R <= p.L ? kFull : valid_rows<R>(m, c * R, p.L);
+      const bool full = inside && bits == kFull;
+      fetch<T, VEC>(to, lx, full, bits, P::zero());
+      fetch<T, VEC>(to + kRowsBytes, lz, full, bits, P::inf());
+      lx.move(kRelay * R), lz.move(kRelay * R);
     }
-  } else {
-    const int ch = c0 + 2 * lane, n = min(max(p.D - ch, 0), 2);
-    const size_t state_at = static_cast<size_t>(b) * p.D + ch;
-    float* saved = p.saved ? p.saved + static_cast<size_t>(b) * chunks * p.D + ch : nullptr;
-    uint64_t h = p.h0 ? load_state<VEC>(p.h0 + state_at, n) : 0ull;
-    int group = 0, slot = 0;
-    for (int c = 0; c < chunks; ++c) {
-      if (saved) store_state<VEC>(saved + static_cast<size_t>(c) * p.D, n, h);
-      uint8_t* his = dynamic + group * kChainGroup;
-      Raw* xs = reinterpret_cast<Raw*>(his + slot * 2 * kRowsBytes) + lane;
-      const uint64_t* ncs = reinterpret_cast<const uint64_t*>(his + kRing * 2 * kRowsBytes) + lane;
-      meet(1 + group);
+    copies_commit();
+    return bits;
+  };
+  uint32_t now = start(w, 0);
+  for (int c = w, slot = 0; c < chunks; c += kRelay, slot ^= 1) {
+    const uint32_t next = start(c + kRelay, slot ^ 1);
+    copies_wait<1>();
+    __syncwarp();
+    uint8_t* rows = mine + slot * 2 * kRowsBytes;
+    Raw* xs = reinterpret_cast<Raw*>(rows) + lane;
+    uint64_t nc[R];
+    row_decays<T, TAU1>(xs + kRowsBytes / sizeof(Raw), p.gate, nc);
+    Join join{f2_both(1.f), 0ull};
 #pragma unroll
-      for (int half = 0; half < R; half += 8) {
-        uint64_t nc[8];
-        Raw x[8];
-#pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          nc[r] = ncs[(half + r) * 32];
-          x[r] = xs[(half + r) * 32];
-        }
-#pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          h = advance<TIED>(h, nc[r], P::f32(x[r]));
-          xs[(half + r) * 32] = P::round(h);
-        }
-      }
-      leave(8 + group);
-      if (++group == kGroups) {
-        group = 0;
-        slot = slot + 1 == kRing ? 0 : slot + 1;
-      }
+    for (int r = 0; r < R; ++r) {
+      join.v = advance<TIED>(join.v, nc[r], P::f32(xs[r * 32]));
+      join.p = f2_fma(nc[r], join.p, join.p);
     }
-    store_state<VEC>(p.last + state_at, n, h);
+    uint64_t h;
+    if (c == 0) {
+      h = p.h0 ? load_state<VEC>(p.h0 + state_at, n) : 0ull;
+    } else {
+      relay_wait(w);
+      h = baton[w][lane];
+    }
+    const uint64_t end = f2_fma(join.p, h, join.v);
+    if (c + 1 < chunks) {
+      const int to = w + 1 == kRelay ? 0 : w + 1;
+      baton[to][lane] = end;
+      relay_pass(to);
+    } else {
+      store_state<VEC>(p.last + state_at, n, end);
+    }
+    if (saved) {
+      store_state<VEC>(saved, n, h);
+      saved += static_cast<size_t>(kRelay) * p.D;
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      h = advance<TIED>(h, nc[r], P::f32(xs[r * 32]));
+      xs[r * 32] = P::round(h);
+    }
+    __syncwarp();
+    put<T, VEC>(rows, lo, inside && now == kFull, min(p.L - c * R, R), now);
+    lo.move(kRelay * R);
+    __syncwarp();
+    now = next;
   }
 }
 
@@ -605,121 +617,94 @@ __device__ __forceinline__ uint64_t input_grad(uint64_t nc, uint64_t g) {
   return TIED ? f2_neg(f2_mul(nc, g)) : g;
 }
 
-// One chain per tile: workers make -c and q in shared memory, the chain warp walks down.
-// -c takes the place of x and z, then dx and dz do.
-constexpr int kWorkers = 7;
-__device__ __forceinline__ void meet_one(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
-__device__ __forceinline__ void leave_one(int id) { asm volatile("bar.arrive %0, 64;" ::"r"(id) : "memory"); }
-constexpr int kBackRing = 2;
-constexpr int kBackWorker = kBackRing * 3 * kRowsBytes + kNcBytes;
-constexpr int kBackShared = kWorkers * kBackWorker;
-
-template <typename T>
-__device__ __forceinline__ void put_nc(typename Pair<T>::Raw* xs, typename Pair<T>::Raw* zs, uint64_t v) {
-  if constexpr (sizeof(T) == 4) {
-    *zs = v;
-  } else {
-    const float2 f = f2_unpack(v);
-    *xs = __float_as_uint(f.x);
-    *zs = __float_as_uint(f.y);
-  }
-}
-template <typename T>
-__device__ __forceinline__ uint64_t get_nc(const typename Pair<T>::Raw* xs, const typename Pair<T>::Raw* zs) {
-  if constexpr (sizeof(T) == 4) return *zs;
-  else return f2_pack(__uint_as_float(*xs), __uint_as_float(*zs));
-}
+// One block per tile, as the forward, with the chunks from the last and the relay going that
+// way: a chunk hands down out = P in + G.
+constexpr int kBackRelay = 9;
+constexpr int kBackRelayShared = kBackRelay * 2 * 3 * kRowsBytes;
 
 template <typename T, bool VEC, bool TAU1, bool TIED>
-__global__ void __launch_bounds__(kWorkers * 32 + 32, 2) scan_chain_backward_kernel(const ScanParams p) {
+__global__ void __launch_bounds__(kBackRelay * 32, 2) scan_relay_backward_kernel(const ScanParams p) {
   using P = Pair<T>;
   using Raw = typename P::Raw;
   constexpr int R = kRowsOf<T>;
+  constexpr uint32_t kFull = (1u << R) - 1u;
   extern __shared__ __align__(128) uint8_t dynamic[];
+  __shared__ uint64_t baton[kBackRelay][32];
   const int w = warp_id(), lane = lane_id(), b = blockIdx.y, c0 = blockIdx.x * 64;
   const int ch = c0 + 2 * lane, n = min(max(p.D - ch, 0), 2);
   const int chunks = (p.L + R - 1) / R;
-  if (w < kWorkers) {
-    uint8_t* mine = dynamic + w * kBackWorker;
-    uint64_t* qs = reinterpret_cast<uint64_t*>(mine + kBackRing * 3 * kRowsBytes) + lane;
-    const uint8_t* m = p.mask ? p.mask + static_cast<size_t>(b) * p.L : nullptr;
-    const float* saved = p.saved + static_cast<size_t>(b) * chunks * p.D + ch;
-    uint64_t state = 0ull;
-    auto start = [&](int k, int slot) {  // the chunk k from the end
-      uint32_t bits = 0;
-      if (k < chunks) {
-        const int c = chunks - 1 - k;
-        bits = valid_rows<R>(m, c * R, p.L);
-        uint8_t* to = mine + slot * 3 * kRowsBytes;
-        fetch<T, VEC>(to, p.x, b, c * R, c0, p.D, bits, P::zero());
-        fetch<T, VEC>(to + kRowsBytes, p.z, b, c * R, c0, p.D, bits, P::inf());
-        fetch<T, VEC>(to + 2 * kRowsBytes, p.dh, b, c * R, c0, p.D, p.dh.ptr ? bits : 0u, P::zero());
-        state = load_state<VEC>(saved + static_cast<size_t>(c) * p.D, n);
-      }
-      copies_commit();
-      return bits;
-    };
-    uint32_t before = 0, now = start(w, 0);
-    int slot = 0;
-    for (int k = w; k < chunks + kWorkers; k += kWorkers, slot ^= 1) {
-      if (k < chunks) copies_wait<0>();
-      if (k >= kWorkers) meet_one(8 + w);
-      __syncwarp();
-      if (k < chunks) {
-        Raw* xs = reinterpret_cast<Raw*>(mine + slot * 3 * kRowsBytes) + lane;
-        Raw* zs = xs + kRowsBytes / sizeof(Raw);
-        uint64_t nc[R], q[R];
-        row_factors<T, TAU1, TIED>(xs, zs, state, p.gate, nc, q);
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          put_nc<T>(xs + r * 32, zs + r * 32, nc[r]);
-          qs[r * 32] = q[r];
-        }
-        leave_one(1 + w);
-      }
-      if (k >= kWorkers) {
-        const uint8_t* done = mine + (slot ^ 1) * 3 * kRowsBytes;
-        const int t0 = (chunks - 1 - (k - kWorkers)) * R;
-        put<T, VEC>(done, p.dx, b, t0, c0, p.D, p.L, before);
-        put<T, VEC>(done + kRowsBytes, p.dz, b, t0, c0, p.D, p.L, before);
-      }
-      __syncwarp();
-      before = now;
-      now = start(k + kWorkers, slot ^ 1);
+  const bool inside = c0 + 64 <= p.D;
+  const size_t state_at = static_cast<size_t>(b) * p.D + ch;
+  const uint8_t* m = p.mask ? p.mask + static_cast<size_t>(b) * p.L : nullptr;
+  uint8_t* mine = dynamic + w * 6 * kRowsBytes;
+  Lane<T, VEC> lx(p.x, b, c0, p.D), lz(p.z, b, c0, p.D), ld(p.dh, b, c0, p.D), ox(p.dx, b, c0, p.D), oz(p.dz, b, c0, p.D);
+  const int first = (chunks - 1 - w) * R;  // below zero where the warp has no chunk: then it is not used
+  lx.move(first), lz.move(first), ld.move(first), ox.move(first), oz.move(first);
+  uint64_t state = 0ull;
+  auto start = [&](int c, int slot) {
+    uint32_t bits = 0;
+    if (c >= 0) {
+      uint8_t* to = mine + slot * 3 * kRowsBytes;
+      bits = !m && (c + 1) * R <= p.L ? kFull : valid_rows<R>(m, c * R, p.L);
+      const bool full = inside && bits == kFull;
+      fetch<T, VEC>(to, lx, full, bits, P::zero());
+      fetch<T, VEC>(to + kRowsBytes, lz, full, bits, P::inf());
+      fetch<T, VEC>(to + 2 * kRowsBytes, ld, full && p.dh.ptr, p.dh.ptr ? bits : 0u, P::zero());
+      lx.move(-kBackRelay * R), lz.move(-kBackRelay * R), ld.move(-kBackRelay * R);
+      state = load_state<VEC>(p.saved + (static_cast<size_t>(b) * chunks + c) * p.D + ch, n);
     }
-  } else {
-    const size_t state_at = static_cast<size_t>(b) * p.D + ch;
-    uint64_t in = p.dlast ? load_state<VEC>(p.dlast + state_at, n) : 0ull;
-    int worker = 0, slot = 0;
-    for (int k = 0; k < chunks; ++k) {
-      uint8_t* his = dynamic + worker * kBackWorker;
-      Raw* xs = reinterpret_cast<Raw*>(his + slot * 3 * kRowsBytes) + lane;
-      Raw* zs = xs + kRowsBytes / sizeof(Raw);
-      const Raw* ds = zs + kRowsBytes / sizeof(Raw);
-      const uint64_t* qs = reinterpret_cast<const uint64_t*>(his + kBackRing * 3 * kRowsBytes) + lane;
-      meet_one(1 + worker);
-      uint64_t nc[R], q[R];
-      Raw d[R];
+    copies_commit();
+    return bits;
+  };
+  uint32_t now = start(chunks - 1 - w, 0);
+  for (int c = chunks - 1 - w, slot = 0; c >= 0; c -= kBackRelay, slot ^= 1) {
+    const uint64_t before = state;
+    const uint32_t next = start(c - kBackRelay, slot ^ 1);
+    copies_wait<1>();
+    __syncwarp();
+    uint8_t* rows = mine + slot * 3 * kRowsBytes;
+    Raw* xs = reinterpret_cast<Raw*>(rows) + lane;
+    Raw* zs = xs + kRowsBytes / sizeof(Raw);
+    const Raw* ds = zs + kRowsBytes / sizeof(Raw);
+    uint64_t nc[R], q[R];
+    row_factors<T, TAU1, TIED>(xs, zs, before, p.gate, nc, q);
+    Join join{f2_both(1.f), 0ull};
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        nc[r] = get_nc<T>(xs + r * 32, zs + r * 32);
-        q[r] = qs[r * 32];
-        d[r] = ds[r * 32];
-      }
-#pragma unroll
-      for (int r = R - 1; r >= 0; --r) {
-        const uint64_t g = f2_add(in, P::f32(d[r]));
-        in = f2_fma(nc[r], g, g);
-        xs[r * 32] = P::round(input_grad<TIED>(nc[r], g));
-        zs[r * 32] = P::round(f2_mul(g, q[r]));
-      }
-      leave_one(8 + worker);
-      if (++worker == kWorkers) {
-        worker = 0;
-        slot ^= 1;
-      }
+    for (int r = R - 1; r >= 0; --r) {
+      join.v = f2_add(join.v, P::f32(ds[r * 32]));
+      join.v = f2_fma(nc[r], join.v, join.v);
+      join.p = f2_fma(nc[r], join.p, join.p);
     }
-    if (p.dh0) store_state<VEC>(p.dh0 + state_at, n, in);
+    uint64_t in;
+    if (c == chunks - 1) {
+      in = p.dlast ? load_state<VEC>(p.dlast + state_at, n) : 0ull;
+    } else {
+      relay_wait(w);
+      in = baton[w][lane];
+    }
+    const uint64_t end = f2_fma(join.p, in, join.v);
+    if (c > 0) {
+      const int to = w + 1 == kBackRelay ? 0 : w + 1;
+      baton[to][lane] = end;
+      relay_pass(to);
+    } else if (p.dh0) {
+      store_state<VEC>(p.dh0 + state_at, n, end);
+    }
+#pragma unroll
+    for (int r = R - 1; r >= 0; --r) {
+      const uint64_t g = f2_add(in, P::f32(ds[r * 32]));
+      in = f2_fma(nc[r], g, g);
+      xs[r * 32] = P::round(input_grad<TIED>(nc[r], g));
+      zs[r * 32] = P::round(f2_mul(g, q[r]));
+    }
+    __syncwarp();
+    const bool full = inside && now == kFull;
+    const int rows_in = min(p.L - c * R, R);
+    put<T, VEC>(rows, ox, full, rows_in, now);
+    put<T, VEC>(rows + kRowsBytes, oz, full, rows_in, now);
+    ox.move(-kBackRelay * R), oz.move(-kBackRelay * R);
+    __syncwarp();
+    now = next;
   }
 }
 
@@ -745,16 +730,21 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_backward_kernel(const Sca
 
   uint32_t coming = 0;
   uint64_t state = 0ull;
+  const bool inside = c0 + 64 <= p.D;
+  Lane<T, VEC> lx(p.x, b, c0, p.D), lz(p.z, b, c0, p.D), ld(p.dh, b, c0, p.D), ox(p.dx, b, c0, p.D), oz(p.dz, b, c0, p.D);
+  const int first = (chunks - 1 - (rank * kWarps + w)) * R, back = -cluster * kWarps * R;
+  lx.move(first), lz.move(first), ld.move(first), ox.move(first), oz.move(first);
   auto start_step = [&](int step) {
     const int c = chunks - 1 - ((step * cluster + rank) * kWarps + w);
     coming = 0;
-    if (step < steps) {
+    if (step < steps) {  // with c < 0 no row is valid and nothing is read
       if (c >= 0) coming = valid_rows<R>(m, c * R, p.L);
       uint8_t* to = mine + (step & 1) * 3 * kRowsBytes;
-      const int t0 = max(c, 0) * R;
-      fetch<T, VEC>(to, p.x, b, t0, c0, p.D, coming, P::zero());
-      fetch<T, VEC>(to + kRowsBytes, p.z, b, t0, c0, p.D, coming, P::inf());
-      fetch<T, VEC>(to + 2 * kRowsBytes, p.dh, b, t0, c0, p.D, p.dh.ptr ? coming : 0u, P::zero());
+      const bool full = inside && coming == (1u << R) - 1u;
+      fetch<T, VEC>(to, lx, full, coming, P::zero());
+      fetch<T, VEC>(to + kRowsBytes, lz, full, coming, P::inf());
+      fetch<T, VEC>(to + 2 * kRowsBytes, ld, full && p.dh.ptr, p.dh.ptr ? coming : 0u, P::zero());
+      lx.move(back), lz.move(back), ld.move(back);
       state = c >= 0 ? load_state<VEC>(saved + static_cast<size_t>(c) * p.D, n) : 0ull;
     }
     copies_commit();
@@ -822,9 +812,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_backward_kernel(const Sca
     }
     __syncwarp();
     if (c >= 0) {
-      put<T, VEC>(rows, p.dx, b, c * R, c0, p.D, p.L, now);
-      put<T, VEC>(rows + kRowsBytes, p.dz, b, c * R, c0, p.D, p.L, now);
+      const bool full = inside && now == (1u << R) - 1u;
+      put<T, VEC>(rows, ox, full, min(p.L - c * R, R), now);
+      put<T, VEC>(rows + kRowsBytes, oz, full, min(p.L - c * R, R), now);
     }
+    ox.move(back), oz.move(back);
   }
   if (p.dh0 && rank == 0 && w == 0) store_state<VEC>(p.dh0 + state_at, n, carry);
 }
@@ -941,7 +933,7 @@ cudaError_t launch_scan_forward(const ScanParams& params, cudaStream_t st) {
     constexpr bool V = decltype(v)::value, U = decltype(u)::value, I = decltype(i)::value;
     if (one_chain(tiles, p.L)) {
       p.cluster = 1;
-      e = launch(scan_chain_kernel<T, V, U, I>, p, kChainThreads, kChainShared, st);
+      e = launch(scan_relay_kernel<T, V, U, I>, p, kRelay * 32, kRelayShared, st);
     } else {
       p.cluster = pick_cluster(tiles, p.L, kWarps * kRowsOf<T>);
       e = launch(scan_forward_kernel<T, V, U, I>, p, kWarps * 32, kForwardRows + (p.cluster > 1 ? p.cluster * kSlots : 0), st);
@@ -965,7 +957,7 @@ cudaError_t launch_scan_backward(const ScanParams& params, cudaStream_t st) {
     constexpr bool V = decltype(v)::value, U = decltype(u)::value, I = decltype(i)::value;
     if (one_chain(tiles, p.L)) {
       p.cluster = 1;
-      e = launch(scan_chain_backward_kernel<T, V, U, I>, p, kWorkers * 32 + 32, kBackShared, st);
+      e = launch(scan_relay_backward_kernel<T, V, U, I>, p, kBackRelay * 32, kBackRelayShared, st);
     } else {
       p.cluster = pick_cluster(tiles, p.L, kWarps * kRowsOf<T>);
       e = launch(scan_backward_kernel<T, V, U, I>, p, kWarps * 32, kBackRows + (p.cluster > 1 ? p.cluster * kSlots : 0), st);
