@@ -379,8 +379,8 @@ int msgla_group_norm_workspace_size(const msgla_norm_config* cfg, long long N, l
  *   M        device uint8 [N, S], nonzero = valid, or NULL. Padded rows enter no
  *            statistic, their output is zero and they are not read.
  *   y        [N, S, C].
- *   stats    f32 [N, groups, 2], mean (0 when center = 0) and 1 / sqrt(var + eps), for
- *            the backward; or NULL.
+ *   stats    f32 [N, groups, 2], 8-byte aligned: mean (0 when center = 0) and
+ *            1 / sqrt(var + eps), for the backward; or NULL.
  *   workspace  msgla_group_norm_workspace_size bytes, 256-byte aligned; calls that may
  *            overlap need one each. NULL when that size is 0. */
 int msgla_group_norm_forward(const msgla_norm_config* cfg, long long N, long long S, const msgla_rows* x,

@@ -6,182 +6,822 @@
 //     dw = sum dv xhat,  db = sum dv,  dgate = dy v act'(gate),
 //     dx = (dv w - <dv w> - xhat <dv w xhat>) / sqrt(var + eps)   (no centring: no <dv w>).
 // Padded rows enter no sum, give zeros and are not read.
+//
+// Bound: HBM. Two forms, by the shape alone:
+// * S = 1 and groups of up to 8192 channels: a team of 1 to 32 lanes, or a block, holds one row's
+//   group in registers, up to 32 values a lane, so every tensor moves once. Teams keep their channels from row to
+//   row: weights stay in registers, and the weight gradients are summed there, joined in
+//   shared memory and written once a block. The next row is loaded while one is computed.
+// * otherwise two passes over blocks of rows and channels: sums first, then the result, which
+//   reads x (and dy) again, from L2 where a pass fits there.
+// Variances are sums of squared differences: from the mean itself in registers, else from each
+// thread's first value, joined by count, mean and sum of squares, so that a mean far
+// from zero costs no digits. Everything is summed in f32 in a fixed order.
+#include <type_traits>
+
 #include "ops_internal.h"
 #include "sm100_ptx.cuh"
 
 namespace msgla {
 namespace {
 
-__device__ __forceinline__ float sigmoid(float v) { return 1.f / (1.f + expf(-v)); }
-__device__ __forceinline__ float act(int kind, float v) {
-  return kind == kActNone ? v : kind == kActSilu ? v * sigmoid(v) : sigmoid(v);
-}
-__device__ __forceinline__ float act_grad(int kind, float v) {
-  if (kind == kActNone) return 1.f;
-  const float s = sigmoid(v);
-  return kind == kActSilu ? s * (1.f + v * (1.f - s)) : s * (1.f - s);
-}
-
 constexpr int kThreads = 256;
+constexpr float kLog2e = 1.4426950408889634f;
 
-// Sum of two values over the block, the same in every thread.
-__device__ __forceinline__ float2 block_sum(float a, float b) {
-  __shared__ float2 part[kThreads / 32];
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    a += __shfl_xor_sync(~0u, a, o);
-    b += __shfl_xor_sync(~0u, b, o);
+__device__ __forceinline__ float sigmoid(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2_approx(-kLog2e * v)));
+  return r;
+}
+__device__ __forceinline__ float act(int kind, float v) {
+  if (kind == kActNone) return v;
+  const float s = sigmoid(v);
+  return kind == kActSilu ? v * s : s;
+}
+// act(v) and act'(v)
+__device__ __forceinline__ float2 act_both(int kind, float v) {
+  if (kind == kActNone) return make_float2(v, 1.f);
+  const float s = sigmoid(v);
+  if (kind == kActSilu) return make_float2(v * s, s * (1.f + v * (1.f - s)));
+  return make_float2(s, s * (1.f - s));
+}
+
+// V neighbouring channels: 16 bytes, or one element where rows are not aligned to 16.
+template <typename T, int V>
+struct Vec {
+  T v[V];
+};
+template <typename T, int V>
+__device__ __forceinline__ Vec<T, V> load(const T* p) {
+  Vec<T, V> r;
+  if constexpr (V == 1) {
+    r.v[0] = *p;
+  } else {
+    static_assert(V * sizeof(T) == 16, "16 bytes");
+    *reinterpret_cast<uint4*>(&r) = __ldg(reinterpret_cast<const uint4*>(p));
   }
-  __syncthreads();
-  if (lane_id() == 0) part[warp_id()] = make_float2(a, b);
-  __syncthreads();
-  a = b = 0.f;
+  return r;
+}
+template <typename T, int V>
+__device__ __forceinline__ Vec<T, V> zeros() {
+  Vec<T, V> r;
 #pragma unroll
-  for (int i = 0; i < kThreads / 32; ++i) {
-    a += part[i].x;
-    b += part[i].y;
+  for (int i = 0; i < V; ++i) r.v[i] = from_f32<T>(0.f);
+  return r;
+}
+template <typename T, int V>
+__device__ __forceinline__ void store(T* p, const Vec<T, V>& r) {
+  if constexpr (V == 1) *p = r.v[0];
+  else *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(&r);
+}
+template <typename T>
+__device__ __forceinline__ T* at(const Rows& r, long long n, long long s, int c) {
+  return static_cast<T*>(r.ptr) + n * r.batch + s * r.row + c;
+}
+
+__device__ __forceinline__ float team_sum(float v, int team) {
+  for (int o = team >> 1; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+  return v;
+}
+// Two sums over a team, or with BLOCK over the whole block (`part`: its warps' sums, two
+// buffers taken in turn so that one barrier a call is enough).
+template <bool BLOCK>
+__device__ __forceinline__ float2 sums_of(float a, float b, int team, float2 (*part)[kThreads / 32], int turn) {
+  a = team_sum(a, BLOCK ? 32 : team);
+  b = team_sum(b, BLOCK ? 32 : team);
+  if constexpr (BLOCK) {
+    if (lane_id() == 0) part[turn][warp_id()] = make_float2(a, b);
+    __syncthreads();
+    a = b = 0.f;
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) {
+      a += part[turn][i].x;
+      b += part[turn][i].y;
+    }
   }
   return make_float2(a, b);
 }
 
-template <typename T>
-__device__ __forceinline__ float value(const Rows& r, long long n, long long s, int c) {
-  return to_f32(static_cast<const T*>(r.ptr)[n * r.batch + s * r.row + c]);
-}
-template <typename T>
-__device__ __forceinline__ void put(const Rows& r, long long n, long long s, int c, float v) {
-  static_cast<T*>(r.ptr)[n * r.batch + s * r.row + c] = from_f32<T>(v);
+// Gradient of the value before the activation, and of the gate.
+__device__ __forceinline__ float grad_v(const NormParams& p, float v, float dy, float gate, float& dgate) {
+  if (!p.gate.ptr) {
+    dgate = 0.f;
+    return dy * act_both(p.act, v).y;
+  }
+  const float2 a = act_both(p.act, gate);
+  dgate = dy * v * a.y;
+  return dy * a.x;
 }
 
-// One block per (n, group).
-template <typename T>
-__global__ void __launch_bounds__(kThreads) norm_forward_kernel(const NormParams p) {
-  const long long n = blockIdx.x / p.G;
-  const int g = blockIdx.x % p.G, cg = p.C / p.G;
-  const long long total = p.S * cg;
-  const uint8_t* m = p.mask ? p.mask + n * p.S : nullptr;
-  float sum = 0.f, count = 0.f;
-  for (long long i = threadIdx.x; i < total; i += kThreads) {
-    const long long s = i / cg;
-    if (m && !m[s]) continue;
-    sum += value<T>(p.x, n, s, g * cg + i % cg);
-    count += 1.f;
-  }
-  const float2 a = block_sum(sum, count);
-  const float n_valid = fmaxf(a.y, 1.f), mean = p.center ? a.x / n_valid : 0.f;
-  float ss = 0.f;
-  for (long long i = threadIdx.x; i < total; i += kThreads) {
-    const long long s = i / cg;
-    if (m && !m[s]) continue;
-    const float d = value<T>(p.x, n, s, g * cg + i % cg) - mean;
-    ss += d * d;
-  }
-  const float rstd = 1.f / sqrtf(block_sum(ss, 0.f).x / n_valid + p.eps);
-  if (p.stats && threadIdx.x == 0) {
-    p.stats[2 * (n * p.G + g)] = mean;
-    p.stats[2 * (n * p.G + g) + 1] = rstd;
-  }
-  for (long long i = threadIdx.x; i < total; i += kThreads) {
-    const long long s = i / cg;
-    const int c = g * cg + i % cg;
-    float y = 0.f;
-    if (!m || m[s]) {
-      float v = (value<T>(p.x, n, s, c) - mean) * rstd;
-      v = v * (p.w ? p.w[c] : 1.f) + (p.b ? p.b[c] : 0.f);
-      y = p.gate.ptr ? v * act(p.act, value<T>(p.gate, n, s, c)) : act(p.act, v);
+// ---------------------------------------------------------------- S = 1: rows in registers
+// Block (slice, y): `gs` groups from slice * gs on, rows (y + k * gridDim.y) * rpi + team / gs.
+struct RowPlan {
+  int team, gs, rpi, slices, blocks;  // threads of a team, groups and rows a block, grid
+};
+
+template <typename T, int V, int NV>
+struct RowLane {
+  int c[NV];    // channels
+  bool in[NV];  // whether they exist
+  int g, row;   // group, and the first row
+  bool active;
+  __device__ __forceinline__ RowLane(const NormParams& p, const RowPlan& q) {
+    const int team = threadIdx.x / q.team, tl = threadIdx.x % q.team, cg = p.C / p.G;
+    g = blockIdx.x * q.gs + team % q.gs;
+    row = team / q.gs;
+    active = row < q.rpi && g < p.G;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int o = (i * q.team + tl) * V;
+      in[i] = active && o < cg;
+      c[i] = g * cg + o;
     }
-    put<T>(p.y, n, s, c, y);
   }
-}
+};
 
-template <typename T>
-__device__ __forceinline__ float grad_v(const NormParams& p, long long n, long long s, int c, float xhat, float& dgate) {
-  const float v = xhat * (p.w ? p.w[c] : 1.f) + (p.b ? p.b[c] : 0.f), dy = value<T>(p.dy, n, s, c);
-  dgate = 0.f;
-  if (!p.gate.ptr) return dy * act_grad(p.act, v);
-  const float gv = value<T>(p.gate, n, s, c);
-  dgate = dy * v * act_grad(p.act, gv);
-  return dy * act(p.act, gv);
-}
-
-template <typename T>
-__global__ void __launch_bounds__(kThreads) norm_backward_kernel(const NormParams p) {
-  const long long n = blockIdx.x / p.G;
-  const int g = blockIdx.x % p.G, cg = p.C / p.G;
-  const long long total = p.S * cg;
-  const uint8_t* m = p.mask ? p.mask + n * p.S : nullptr;
-  const float mean = p.stats[2 * (n * p.G + g)], rstd = p.stats[2 * (n * p.G + g) + 1];
-  float s1 = 0.f, s2 = 0.f, count = 0.f, dg;
-  for (long long i = threadIdx.x; i < total; i += kThreads) {
-    const long long s = i / cg;
-    if (m && !m[s]) continue;
-    const int c = g * cg + i % cg;
-    const float xhat = (value<T>(p.x, n, s, c) - mean) * rstd;
-    const float d = grad_v<T>(p, n, s, c, xhat, dg) * (p.w ? p.w[c] : 1.f);
-    s1 += d;
-    s2 += d * xhat;
-    count += 1.f;
-  }
-  const float2 a = block_sum(s1, s2);
-  const float inv = 1.f / fmaxf(block_sum(count, 0.f).x, 1.f);
-  const float m1 = p.center ? a.x * inv : 0.f, m2 = a.y * inv;
-  for (long long i = threadIdx.x; i < total; i += kThreads) {
-    const long long s = i / cg;
-    const int c = g * cg + i % cg;
-    float dx = 0.f;
-    dg = 0.f;
-    if (!m || m[s]) {
-      const float xhat = (value<T>(p.x, n, s, c) - mean) * rstd;
-      const float d = grad_v<T>(p, n, s, c, xhat, dg) * (p.w ? p.w[c] : 1.f);
-      dx = (d - m1 - xhat * m2) * rstd;
+template <typename T, int V, int NV, bool BLOCK>
+__global__ void __launch_bounds__(kThreads) norm_rows_forward_kernel(const NormParams p, const RowPlan q) {
+  __shared__ float2 part[2][kThreads / 32];
+  constexpr bool kKeep = V * NV <= 16;  // weights in registers
+  const RowLane<T, V, NV> l(p, q);
+  const float inv = 1.f / (p.C / p.G);
+  const bool gated = p.gate.ptr;
+  float w[kKeep ? NV : 1][V], b[kKeep ? NV : 1][V];
+  auto weights = [&](int i, float (&wi)[V], float (&bi)[V]) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      wi[e] = p.w && l.in[i] ? __ldg(p.w + l.c[i] + e) : 1.f;
+      bi[e] = p.b && l.in[i] ? __ldg(p.b + l.c[i] + e) : 0.f;
     }
-    put<T>(p.dx, n, s, c, dx);
-    if (p.gate.ptr) put<T>(p.dgate, n, s, c, dg);
+  };
+  if constexpr (kKeep) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) weights(i, w[i], b[i]);
+  }
+  const long long step = static_cast<long long>(gridDim.y) * q.rpi;
+  Vec<T, V> xn[NV], gn[NV];
+  bool valid_next;
+  auto fetch = [&](long long row) {
+    valid_next = l.active && row < p.N && (!p.mask || p.mask[row]);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      xn[i] = valid_next && l.in[i] ? load<T, V>(at<T>(p.x, row, 0, l.c[i])) : zeros<T, V>();
+      gn[i] = valid_next && l.in[i] && gated ? load<T, V>(at<T>(p.gate, row, 0, l.c[i])) : zeros<T, V>();
+    }
+  };
+  long long row = static_cast<long long>(blockIdx.y) * q.rpi + l.row;
+  fetch(row);
+  for (long long base = static_cast<long long>(blockIdx.y) * q.rpi; base < p.N; base += step, row += step) {
+    float x[NV][V];
+    Vec<T, V> gt[NV];
+    const bool valid = valid_next;
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      gt[i] = gn[i];
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        x[i][e] = to_f32(xn[i].v[e]);
+        sum += x[i][e];
+      }
+    }
+    if (base + step < p.N) fetch(row + step);
+    const float mean = p.center ? sums_of<BLOCK>(sum, 0.f, q.team, part, 0).x * inv : 0.f;
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        x[i][e] = l.in[i] ? x[i][e] - mean : 0.f;
+        ss = fmaf(x[i][e], x[i][e], ss);
+      }
+    const float rstd = 1.f / sqrtf(sums_of<BLOCK>(ss, 0.f, q.team, part, 1).x * inv + p.eps);
+    if (BLOCK && !p.center) __syncthreads();  // the next row writes the same buffer
+    if (!l.active || row >= p.N) continue;
+    if (p.stats && threadIdx.x % q.team == 0)
+      *reinterpret_cast<float2*>(p.stats + 2 * (row * p.G + l.g)) = make_float2(mean, rstd);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (!l.in[i]) continue;
+      float wl[V], bl[V];
+      if constexpr (!kKeep) weights(i, wl, bl);
+      Vec<T, V> y;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float v = fmaf(x[i][e] * rstd, kKeep ? w[kKeep ? i : 0][e] : wl[e], kKeep ? b[kKeep ? i : 0][e] : bl[e]);
+        const float r = gated ? v * act(p.act, to_f32(gt[i].v[e])) : act(p.act, v);
+        y.v[e] = from_f32<T>(valid ? r : 0.f);
+      }
+      store<T, V>(at<T>(p.y, row, 0, l.c[i]), y);
+    }
   }
 }
 
-// One block per channel: dw and db over all rows.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) norm_weight_kernel(const NormParams p) {
-  const int c = blockIdx.x, g = c / (p.C / p.G);
-  float s1 = 0.f, s2 = 0.f, dg;
-  for (long long i = threadIdx.x; i < p.N * p.S; i += kThreads) {
-    const long long n = i / p.S, s = i % p.S;
-    if (p.mask && !p.mask[i]) continue;
-    const float* st = p.stats + 2 * (n * p.G + g);
-    const float xhat = (value<T>(p.x, n, s, c) - st[0]) * st[1], d = grad_v<T>(p, n, s, c, xhat, dg);
-    s1 += d * xhat;
-    s2 += d;
+// Weight gradients: partial sums [blocks][2][C] (dw, db) in the workspace.
+template <typename T, int V, int NV, bool BLOCK>
+__global__ void __launch_bounds__(kThreads) norm_rows_backward_kernel(const NormParams p, const RowPlan q) {
+  __shared__ float2 part[2][kThreads / 32];
+  int turn = 0;
+  extern __shared__ float shared[];  // [rpi - 1][gs * cg][2]
+  const RowLane<T, V, NV> l(p, q);
+  const int cg = p.C / p.G;
+  const float inv = 1.f / cg;
+  const bool gated = p.gate.ptr;
+  float dw[NV][V] = {}, db[NV][V] = {};
+  const long long step = static_cast<long long>(gridDim.y) * q.rpi;
+  Vec<T, V> xn[NV], dn[NV], gn[NV];
+  float2 sn;
+  bool valid_next;
+  auto fetch = [&](long long row) {
+    valid_next = l.active && row < p.N && (!p.mask || p.mask[row]);
+    sn = valid_next ? *reinterpret_cast<const float2*>(p.stats + 2 * (row * p.G + l.g)) : make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const bool in = valid_next && l.in[i];
+      xn[i] = in ? load<T, V>(at<T>(p.x, row, 0, l.c[i])) : zeros<T, V>();
+      dn[i] = in ? load<T, V>(at<T>(p.dy, row, 0, l.c[i])) : zeros<T, V>();
+      gn[i] = in && gated ? load<T, V>(at<T>(p.gate, row, 0, l.c[i])) : zeros<T, V>();
+    }
+  };
+  long long row = static_cast<long long>(blockIdx.y) * q.rpi + l.row;
+  fetch(row);
+  for (long long base = static_cast<long long>(blockIdx.y) * q.rpi; base < p.N; base += step, row += step) {
+    Vec<T, V> x[NV], d[NV], gt[NV];
+    const float2 st = sn;
+    const bool valid = valid_next, here = l.active && row < p.N;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      x[i] = xn[i];
+      d[i] = dn[i];
+      gt[i] = gn[i];
+    }
+    if (base + step < p.N) fetch(row + step);
+    float s1 = 0.f, s2 = 0.f, xh[NV][V], dv[NV][V];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      Vec<T, V> dg;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const bool in = valid && l.in[i];
+        const float w = p.w && l.in[i] ? __ldg(p.w + l.c[i] + e) : 1.f, b = p.b && l.in[i] ? __ldg(p.b + l.c[i] + e) : 0.f;
+        xh[i][e] = in ? (to_f32(x[i].v[e]) - st.x) * st.y : 0.f;
+        float g;
+        const float t = in ? grad_v(p, fmaf(xh[i][e], w, b), to_f32(d[i].v[e]), to_f32(gt[i].v[e]), g) : g = 0.f;
+        dg.v[e] = from_f32<T>(g);
+        dw[i][e] = fmaf(t, xh[i][e], dw[i][e]);
+        db[i][e] += t;
+        dv[i][e] = t * w;
+        s1 += dv[i][e];
+        s2 = fmaf(dv[i][e], xh[i][e], s2);
+      }
+      if (gated && here && l.in[i]) store<T, V>(at<T>(p.dgate, row, 0, l.c[i]), dg);
+    }
+    const float2 sums = sums_of<BLOCK>(s1, s2, q.team, part, turn ^= 1);
+    const float m1 = p.center ? sums.x * inv : 0.f, m2 = sums.y * inv;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      Vec<T, V> dx;
+#pragma unroll
+      for (int e = 0; e < V; ++e) dx.v[e] = from_f32<T>(valid ? (dv[i][e] - m1 - xh[i][e] * m2) * st.y : 0.f);
+      if (here && l.in[i]) store<T, V>(at<T>(p.dx, row, 0, l.c[i]), dx);
+    }
   }
-  const float2 a = block_sum(s1, s2);
-  if (threadIdx.x == 0) {
-    if (p.dw) p.dw[c] = a.x;
-    if (p.db) p.db[c] = a.y;
+  if (!p.dw && !p.db) return;
+  // the block's rows of every channel, summed in order by the first one's team
+  const int width = q.gs * cg, c0 = blockIdx.x * width;
+  if (l.active && l.row > 0) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (l.in[i])
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+          *reinterpret_cast<float2*>(shared + 2 * ((l.row - 1) * width + l.c[i] + e - c0)) = make_float2(dw[i][e], db[i][e]);
+  }
+  __syncthreads();
+  if (!l.active || l.row > 0) return;
+  float* out = static_cast<float*>(p.workspace) + static_cast<size_t>(blockIdx.y) * 2 * p.C;
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+    if (l.in[i])
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        float2 s = make_float2(dw[i][e], db[i][e]);
+        for (int r = 1; r < q.rpi; ++r) {
+          const float2 o = *reinterpret_cast<const float2*>(shared + 2 * ((r - 1) * width + l.c[i] + e - c0));
+          s.x += o.x;
+          s.y += o.y;
+        }
+        out[l.c[i] + e] = s.x;
+        out[p.C + l.c[i] + e] = s.y;
+      }
+}
+
+// dw and db from `rows` partial sums [rows][2][C]. 32 channels a block.
+__global__ void __launch_bounds__(1024) norm_weights_kernel(const NormParams p, const float* part, int rows) {
+  __shared__ float2 sums[32][33];
+  const int c = blockIdx.x * 32 + threadIdx.x;
+  float2 s = make_float2(0.f, 0.f);
+  if (c < p.C)
+    for (int r = threadIdx.y; r < rows; r += 32) {
+      const float* f = part + static_cast<size_t>(r) * 2 * p.C + c;
+      s.x += f[0];
+      s.y += f[p.C];
+    }
+  sums[threadIdx.y][threadIdx.x] = s;
+  __syncthreads();
+  s = sums[threadIdx.x][threadIdx.y];  // the 32 partial sums of one channel, in one warp
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    s.x += __shfl_xor_sync(~0u, s.x, o);
+    s.y += __shfl_xor_sync(~0u, s.y, o);
+  }
+  const int co = blockIdx.x * 32 + threadIdx.y;
+  if (threadIdx.x == 0 && co < p.C) {
+    if (p.dw) p.dw[co] = s.x;
+    if (p.db) p.db[co] = s.y;
   }
 }
+
+// ---------------------------------------------------------------- blocks of rows and channels
+// Block (n, chunk, tile): `ty` rows at a time of tx vectors of channels. Workspace: per (n,
+// chunk) and segment (the part of a group inside a tile) two numbers at the segment's first
+// channel; with gradients also per channel.
+struct BlockPlan {
+  int tx, ty, width;  // threads along channels and rows, channels a tile
+  int tiles, chunks, rows;  // rows a chunk
+};
+
+struct Part {
+  long long n;
+  int chunk, tile;
+  __device__ __forceinline__ explicit Part(const BlockPlan& q) {
+    unsigned i = blockIdx.x;
+    tile = i % q.tiles;
+    i /= q.tiles;
+    chunk = i % q.chunks;
+    n = i / q.chunks;
+  }
+};
+
+// Forward sums: float2 (mean, sum of squared differences) per segment at
+// seg[(n * chunks + chunk) * C + channel]; the valid rows of each (n, chunk) at rows_of.
+template <typename T, int V>
+__global__ void __launch_bounds__(kThreads) norm_sums_kernel(const NormParams p, const BlockPlan q, float2* seg, float* rows_of) {
+  extern __shared__ float2 cell[];  // [ty][width]
+  __shared__ int counts[kThreads];
+  const Part part(q);
+  const int tx = threadIdx.x % q.tx, ty = threadIdx.x / q.tx, c = part.tile * q.width + tx * V, cg = p.C / p.G;
+  const long long s0 = static_cast<long long>(part.chunk) * q.rows, s1 = min(s0 + q.rows, p.S);
+  const uint8_t* m = p.mask ? p.mask + part.n * p.S : nullptr;
+  float first[V] = {}, sum[V] = {}, sq[V] = {};
+  int count = 0;
+  if (c < p.C)
+    for (long long s = s0 + ty; s < s1; s += q.ty) {
+      if (m && !m[s]) continue;
+      const Vec<T, V> x = load<T, V>(at<T>(p.x, part.n, s, c));
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float v = to_f32(x.v[e]);
+        if (count == 0) first[e] = p.center ? v : 0.f;
+        const float d = v - first[e];
+        sum[e] += d;
+        sq[e] = fmaf(d, d, sq[e]);
+      }
+      ++count;
+    }
+  const float n = static_cast<float>(max(count, 1));
+#pragma unroll
+  for (int e = 0; e < V; ++e)
+    if (c < p.C) {
+      const float mean = sum[e] / n;
+      cell[ty * q.width + tx * V + e] = make_float2(p.center ? first[e] + mean : 0.f, p.center ? fmaxf(sq[e] - sum[e] * mean, 0.f) : sq[e]);
+    }
+  if (tx == 0) counts[ty] = count;
+  __syncthreads();
+  int rows = 0;
+  for (int r = 0; r < q.ty; ++r) rows += counts[r];
+  if (part.tile == 0 && threadIdx.x == 0) rows_of[part.n * q.chunks + part.chunk] = static_cast<float>(rows);
+  // one warp joins a segment: its mean, then the squares about it
+  const int t0 = part.tile * q.width, t1 = min(t0 + q.width, p.C);
+  for (int g = t0 / cg + warp_id(); g * cg < t1; g += kThreads / 32) {
+    const int a = max(g * cg, t0), wide = min((g + 1) * cg, t1) - a, cells = wide * q.ty;
+    float total = 0.f, squares = 0.f, base = 0.f, mean = 0.f;
+    if (p.center && rows) {
+      int r0 = 0;
+      while (counts[r0] == 0) ++r0;
+      base = cell[r0 * q.width + a - t0].x;
+      for (int i = lane_id(); i < cells; i += 32) {
+        const int r = i / wide;
+        if (counts[r]) total += counts[r] * (cell[r * q.width + a - t0 + i % wide].x - base);
+      }
+      mean = base + team_sum(total, 32) / (static_cast<float>(rows) * wide);
+    }
+    for (int i = lane_id(); i < cells; i += 32) {
+      const int r = i / wide;
+      if (!counts[r]) continue;
+      const float2 v = cell[r * q.width + a - t0 + i % wide];
+      const float d = v.x - mean;
+      squares += v.y + counts[r] * d * d;
+    }
+    squares = team_sum(squares, 32);
+    if (lane_id() == 0) seg[(part.n * q.chunks + part.chunk) * p.C + a] = make_float2(mean, squares);
+  }
+}
+
+// Joins the segments of group g of sample n (one warp): mean and 1 / sqrt(var + eps), in every lane.
+__device__ __forceinline__ float2 join_stats(const NormParams& p, const BlockPlan& q, long long n, int g, const float2* seg,
+                                             const float* rows_of) {
+  const int cg = p.C / p.G, a = g * cg, t0 = a / q.width, segs = (a + cg - 1) / q.width - t0 + 1;
+  auto get = [&](int i, float& count) {
+    const int chunk = i / segs, t = t0 + i % segs, lo = max(a, t * q.width), hi = min(a + cg, (t + 1) * q.width);
+    count = rows_of[n * q.chunks + chunk] * (hi - lo);
+    return seg[(n * q.chunks + chunk) * p.C + lo];
+  };
+  const int all = segs * q.chunks;
+  float count = 0.f, total = 0.f, squares = 0.f, k;
+  float base = 0.f;
+  if (p.center) {  // some segment with rows, as the point to sum differences from
+    for (int i = 0; i < all; ++i) {
+      const float2 v = get(i, k);
+      if (k > 0.f) {
+        base = v.x;
+        break;
+      }
+    }
+  }
+  for (int i = lane_id(); i < all; i += 32) {
+    const float2 v = get(i, k);
+    count += k;
+    if (k > 0.f) total = fmaf(k, v.x - base, total);
+  }
+  count = fmaxf(team_sum(count, 32), 1.f);
+  const float mean = p.center ? base + team_sum(total, 32) / count : 0.f;
+  for (int i = lane_id(); i < all; i += 32) {
+    const float2 v = get(i, k);
+    const float d = v.x - mean;
+    if (k > 0.f) squares += v.y + k * d * d;
+  }
+  return make_float2(mean, 1.f / sqrtf(team_sum(squares, 32) / count + p.eps));
+}
+
+template <typename T, int V>
+__global__ void __launch_bounds__(kThreads) norm_apply_kernel(const NormParams p, const BlockPlan q, const float2* seg,
+                                                              const float* rows_of) {
+  extern __shared__ float2 stat[];  // groups that meet the tile
+  const Part part(q);
+  const int tx = threadIdx.x % q.tx, ty = threadIdx.x / q.tx, c = part.tile * q.width + tx * V, cg = p.C / p.G;
+  const int t0 = part.tile * q.width, t1 = min(t0 + q.width, p.C), g0 = t0 / cg;
+  for (int g = g0 + warp_id(); g * cg < t1; g += kThreads / 32) {
+    const float2 v = join_stats(p, q, part.n, g, seg, rows_of);
+    if (lane_id() == 0) {
+      stat[g - g0] = v;
+      if (p.stats && part.chunk == 0 && g * cg >= t0) *reinterpret_cast<float2*>(p.stats + 2 * (part.n * p.G + g)) = v;
+    }
+  }
+  __syncthreads();
+  if (c >= p.C) return;
+  float mean[V], w[V], b[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    const float2 v = stat[(c + e) / cg - g0];
+    mean[e] = v.x;
+    w[e] = v.y * (p.w ? p.w[c + e] : 1.f);
+    b[e] = p.b ? p.b[c + e] : 0.f;
+  }
+  const long long s0 = static_cast<long long>(part.chunk) * q.rows, s1 = min(s0 + q.rows, p.S);
+  const uint8_t* m = p.mask ? p.mask + part.n * p.S : nullptr;
+  for (long long s = s0 + ty; s < s1; s += q.ty) {
+    Vec<T, V> y = zeros<T, V>();
+    if (!m || m[s]) {
+      const Vec<T, V> x = load<T, V>(at<T>(p.x, part.n, s, c));
+      const Vec<T, V> gt = p.gate.ptr ? load<T, V>(at<T>(p.gate, part.n, s, c)) : x;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float v = fmaf(to_f32(x.v[e]) - mean[e], w[e], b[e]);
+        y.v[e] = from_f32<T>(p.gate.ptr ? v * act(p.act, to_f32(gt.v[e])) : act(p.act, v));
+      }
+    }
+    store<T, V>(at<T>(p.y, part.n, s, c), y);
+  }
+}
+
+// Backward sums: per channel dw and db of every (n, chunk) as chan[(n * chunks + chunk)][2][C], per
+// segment (sum dv w, sum dv w xhat) as seg, and the valid rows.
+template <typename T, int V>
+__global__ void __launch_bounds__(kThreads) norm_grad_sums_kernel(const NormParams p, const BlockPlan q, float* chan, float2* seg,
+                                                                  float* rows_of) {
+  extern __shared__ float2 cell[];  // [ty][width]
+  __shared__ int counts[kThreads];
+  const Part part(q);
+  const int tx = threadIdx.x % q.tx, ty = threadIdx.x / q.tx, c = part.tile * q.width + tx * V, cg = p.C / p.G;
+  const long long s0 = static_cast<long long>(part.chunk) * q.rows, s1 = min(s0 + q.rows, p.S);
+  const uint8_t* m = p.mask ? p.mask + part.n * p.S : nullptr;
+  const size_t at_part = static_cast<size_t>(part.n) * q.chunks + part.chunk;
+  float mean[V], rstd[V], w[V], b[V], dw[V] = {}, db[V] = {};
+  int count = 0;
+  if (c < p.C) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const float2 v = *reinterpret_cast<const float2*>(p.stats + 2 * (part.n * p.G + (c + e) / cg));
+      mean[e] = v.x;
+      rstd[e] = v.y;
+      w[e] = p.w ? p.w[c + e] : 1.f;
+      b[e] = p.b ? p.b[c + e] : 0.f;
+    }
+    for (long long s = s0 + ty; s < s1; s += q.ty) {
+      if (m && !m[s]) continue;
+      ++count;
+      const Vec<T, V> x = load<T, V>(at<T>(p.x, part.n, s, c)), d = load<T, V>(at<T>(p.dy, part.n, s, c));
+      const Vec<T, V> gt = p.gate.ptr ? load<T, V>(at<T>(p.gate, part.n, s, c)) : x;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float xh = (to_f32(x.v[e]) - mean[e]) * rstd[e];
+        float dg;
+        const float t = grad_v(p, fmaf(xh, w[e], b[e]), to_f32(d.v[e]), to_f32(gt.v[e]), dg);
+        dw[e] = fmaf(t, xh, dw[e]);
+        db[e] += t;
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) cell[ty * q.width + tx * V + e] = make_float2(dw[e], db[e]);
+  }
+  if (tx == 0) counts[ty] = count;
+  __syncthreads();
+  if (part.tile == 0 && threadIdx.x == 0) {
+    int rows = 0;
+    for (int r = 0; r < q.ty; ++r) rows += counts[r];
+    rows_of[at_part] = static_cast<float>(rows);
+  }
+  const int t0 = part.tile * q.width, t1 = min(t0 + q.width, p.C);
+  for (int i = threadIdx.x; i < t1 - t0; i += kThreads) {
+    float2 s = cell[i];
+    for (int r = 1; r < q.ty; ++r) {
+      s.x += cell[r * q.width + i].x;
+      s.y += cell[r * q.width + i].y;
+    }
+    if (p.dw || p.db) {
+      chan[at_part * 2 * p.C + t0 + i] = s.x;
+      chan[at_part * 2 * p.C + p.C + t0 + i] = s.y;
+    }
+    const float wi = p.w ? p.w[t0 + i] : 1.f;
+    cell[i] = make_float2(s.y * wi, s.x * wi);
+  }
+  __syncthreads();
+  for (int g = t0 / cg + warp_id(); g * cg < t1; g += kThreads / 32) {
+    const int a = max(g * cg, t0), wide = min((g + 1) * cg, t1) - a;
+    float s1v = 0.f, s2v = 0.f;
+    for (int i = lane_id(); i < wide; i += 32) {
+      s1v += cell[a - t0 + i].x;
+      s2v += cell[a - t0 + i].y;
+    }
+    s1v = team_sum(s1v, 32);
+    s2v = team_sum(s2v, 32);
+    if (lane_id() == 0) seg[at_part * p.C + a] = make_float2(s1v, s2v);
+  }
+}
+
+template <typename T, int V>
+__global__ void __launch_bounds__(kThreads) norm_grad_apply_kernel(const NormParams p, const BlockPlan q, const float2* seg,
+                                                                   const float* rows_of) {
+  extern __shared__ float2 stat[];  // <dv w>, <dv w xhat> of the groups that meet the tile
+  const Part part(q);
+  const int tx = threadIdx.x % q.tx, ty = threadIdx.x / q.tx, c = part.tile * q.width + tx * V, cg = p.C / p.G;
+  const int t0 = part.tile * q.width, t1 = min(t0 + q.width, p.C), g0 = t0 / cg;
+  for (int g = g0 + warp_id(); g * cg < t1; g += kThreads / 32) {
+    const int a = g * cg, first = a / q.width, segs = (a + cg - 1) / q.width - first + 1;
+    float s1v = 0.f, s2v = 0.f, count = 0.f;
+    for (int i = lane_id(); i < segs * q.chunks; i += 32) {
+      const size_t row = static_cast<size_t>(part.n) * q.chunks + i / segs;
+      const float2 v = seg[row * p.C + max(a, (first + i % segs) * q.width)];
+      s1v += v.x;
+      s2v += v.y;
+      if (i % segs == 0) count += rows_of[row];
+    }
+    s1v = team_sum(s1v, 32);
+    s2v = team_sum(s2v, 32);
+    count = fmaxf(team_sum(count, 32), 1.f) * cg;
+    if (lane_id() == 0) stat[g - g0] = make_float2(p.center ? s1v / count : 0.f, s2v / count);
+  }
+  __syncthreads();
+  if (c >= p.C) return;
+  float mean[V], rstd[V], w[V], b[V], m1[V], m2[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    const int g = (c + e) / cg;
+    const float2 v = *reinterpret_cast<const float2*>(p.stats + 2 * (part.n * p.G + g));
+    mean[e] = v.x;
+    rstd[e] = v.y;
+    w[e] = p.w ? p.w[c + e] : 1.f;
+    b[e] = p.b ? p.b[c + e] : 0.f;
+    m1[e] = stat[g - g0].x;
+    m2[e] = stat[g - g0].y;
+  }
+  const long long s0 = static_cast<long long>(part.chunk) * q.rows, s1 = min(s0 + q.rows, p.S);
+  const uint8_t* m = p.mask ? p.mask + part.n * p.S : nullptr;
+  for (long long s = s0 + ty; s < s1; s += q.ty) {
+    Vec<T, V> dx = zeros<T, V>(), dgate = dx;
+    if (!m || m[s]) {
+      const Vec<T, V> x = load<T, V>(at<T>(p.x, part.n, s, c)), d = load<T, V>(at<T>(p.dy, part.n, s, c));
+      const Vec<T, V> gt = p.gate.ptr ? load<T, V>(at<T>(p.gate, part.n, s, c)) : x;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float xh = (to_f32(x.v[e]) - mean[e]) * rstd[e];
+        float dg;
+        const float t = grad_v(p, fmaf(xh, w[e], b[e]), to_f32(d.v[e]), to_f32(gt.v[e]), dg) * w[e];
+        dx.v[e] = from_f32<T>((t - m1[e] - xh * m2[e]) * rstd[e]);
+        dgate.v[e] = from_f32<T>(dg);
+      }
+    }
+    store<T, V>(at<T>(p.dx, part.n, s, c), dx);
+    if (p.gate.ptr) store<T, V>(at<T>(p.dgate, part.n, s, c), dgate);
+  }
+}
+
+// ---------------------------------------------------------------- plans and launches
+int multiprocessors() {
+  int dev = 0, n = 148;
+  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+  return n;
+}
+
+bool aligned16(const Rows& r, int dtype) {
+  const int run = dtype == kF32 ? 4 : 8;
+  return !r.ptr || (reinterpret_cast<uintptr_t>(r.ptr) % 16 == 0 && r.batch % run == 0 && r.row % run == 0);
+}
+
+// Elements an access takes: 16 bytes where every row of every tensor allows it.
+int vector_of(const NormParams& p) {
+  const int run = p.dtype == kF32 ? 4 : 8;
+  const bool ok = p.C / p.G % run == 0 && aligned16(p.x, p.dtype) && aligned16(p.gate, p.dtype) && aligned16(p.y, p.dtype) &&
+                  aligned16(p.dy, p.dtype) && aligned16(p.dx, p.dtype) && aligned16(p.dgate, p.dtype);
+  return ok ? run : 1;
+}
+
+// Values of a row a lane holds at most: 32, or 16 where they are loaded one by one.
+int lane_values(int v) { return v == 1 ? 16 : 32; }
+bool rows_form(const NormParams& p, int v) { return p.S == 1 && p.C / p.G <= kThreads * lane_values(v); }
+
+RowPlan row_plan(const NormParams& p, int v, int per_sm) {
+  const int vectors = (p.C / p.G + v - 1) / v;
+  RowPlan q;
+  q.team = 1;
+  while (q.team < 32 && q.team < vectors) q.team *= 2;
+  if (p.C / p.G > 32 * lane_values(v)) q.team = kThreads;
+  const int teams = kThreads / q.team;
+  q.gs = p.G < teams ? p.G : teams;
+  q.rpi = teams / q.gs;
+  q.slices = (p.G + q.gs - 1) / q.gs;
+  const long long most = (p.N + q.rpi - 1) / q.rpi;
+  const long long want = (static_cast<long long>(multiprocessors()) * per_sm + q.slices - 1) / q.slices;
+  q.blocks = static_cast<int>(most < want ? most : want);
+  if (q.blocks > 65535) q.blocks = 65535;
+  return q;
+}
+
+// Rows and channels of a block: as many rows at once as there are, up to 32, and chunks so that a
+// thread sums at most 64 rows and the GPU has several blocks an SM.
+BlockPlan block_plan(const NormParams& p, int v) {
+  BlockPlan q;
+  q.ty = 1;
+  while (q.ty < 32 && q.ty < p.S) q.ty *= 2;
+  q.tx = kThreads / q.ty;
+  while (q.tx > 1 && (q.tx / 2) * v >= p.C && q.ty < kThreads) q.tx /= 2, q.ty *= 2;
+  q.width = q.tx * v;
+  q.tiles = (p.C + q.width - 1) / q.width;
+  const long long blocks = p.N * q.tiles, rows_at_once = (p.S + q.ty - 1) / q.ty;
+  long long chunks = (8LL * multiprocessors() + blocks - 1) / blocks;
+  const long long least = (rows_at_once + 63) / 64, most = rows_at_once < 512 ? rows_at_once : 512;
+  if (chunks < least) chunks = least;
+  if (chunks > most) chunks = most;
+  q.rows = static_cast<int>((rows_at_once + chunks - 1) / chunks) * q.ty;
+  q.chunks = static_cast<int>((p.S + q.rows - 1) / q.rows);
+  return q;
+}
+
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+// Workspace of the block form: segments, valid rows, and with gradients the channels' sums.
+struct BlockSpace {
+  float2* seg;
+  float *rows_of, *chan;
+  size_t bytes;
+  BlockSpace(const NormParams& p, const BlockPlan& q, bool backward) {
+    const size_t parts = static_cast<size_t>(p.N) * q.chunks;
+    uint8_t* at = static_cast<uint8_t*>(p.workspace);
+    seg = reinterpret_cast<float2*>(at);
+    const size_t a = round256(parts * p.C * 8), b = round256(parts * 4);
+    rows_of = reinterpret_cast<float*>(at + a);
+    chan = reinterpret_cast<float*>(at + a + b);
+    bytes = a + b + (backward ? round256(parts * p.C * 8) : 0);
+  }
+};
 
 template <typename F>
-void by_dtype(int dtype, F&& f) {
-  if (dtype == kBF16) f(__nv_bfloat16{});
-  else if (dtype == kF16) f(__half{});
-  else f(float{});
+void by_type(int dtype, int v, F&& f) {
+  auto by_vec = [&](auto t) {
+    if (v == 1) f(t, std::integral_constant<int, 1>{});
+    else f(t, std::integral_constant<int, 16 / sizeof(t)>{});
+  };
+  if (dtype == kBF16) by_vec(__nv_bfloat16{});
+  else if (dtype == kF16) by_vec(__half{});
+  else by_vec(float{});
+}
+// f(vectors a lane, BLOCK) for the smallest number that holds a group
+template <int V, typename F>
+void by_vectors(const NormParams& p, const RowPlan& q, F&& f) {
+  const int need = (p.C / p.G + q.team * V - 1) / (q.team * V);
+  auto with = [&](auto nv) {
+    if (q.team > 32) f(nv, std::true_type{});
+    else f(nv, std::false_type{});
+  };
+  if (need <= 1) with(std::integral_constant<int, 1>{});
+  else if (need <= 2) with(std::integral_constant<int, 2>{});
+  else if (need <= 4) with(std::integral_constant<int, 4>{});
+  else if constexpr (V <= 4) {
+    if (need <= 8) with(std::integral_constant<int, 8>{});
+    else if constexpr (V == 1) with(std::integral_constant<int, 16>{});
+  }
+}
+
+constexpr int kRowBlocks = 4, kRowBlocksBackward = 2;  // blocks an SM of the rows form
+
+void launch_weights(const NormParams& p, const float* part, int rows, cudaStream_t st) {
+  if (p.dw || p.db) norm_weights_kernel<<<(p.C + 31) / 32, dim3(32, 32), 0, st>>>(p, part, rows);
 }
 
 }  // namespace
 
-size_t norm_workspace(const NormParams&, bool) { return 0; }
+// The workspace must not depend on alignment, which the size query does not know: the larger of both forms.
+size_t norm_workspace(const NormParams& p, bool backward) {
+  size_t most = 0;
+  for (int v : {1, p.dtype == kF32 ? 4 : 8}) {
+    if (v > 1 && p.C / p.G % v) continue;
+    size_t n;
+    if (rows_form(p, v)) {
+      n = backward ? static_cast<size_t>(row_plan(p, v, kRowBlocksBackward).blocks) * 2 * p.C * 4 : 0;
+    } else {
+      n = BlockSpace(p, block_plan(p, v), backward).bytes;
+    }
+    most = n > most ? n : most;
+  }
+  return most;
+}
 
 cudaError_t launch_norm_forward(const NormParams& p, cudaStream_t st) {
-  by_dtype(p.dtype, [&](auto t) { norm_forward_kernel<decltype(t)><<<unsigned(p.N * p.G), kThreads, 0, st>>>(p); });
-  return cudaGetLastError();
+  const int v = vector_of(p);
+  cudaError_t e = cudaSuccess;
+  by_type(p.dtype, v, [&](auto t, auto vec) {
+    using T = decltype(t);
+    constexpr int V = decltype(vec)::value;
+    if (rows_form(p, v)) {
+      const RowPlan q = row_plan(p, v, kRowBlocks);
+      by_vectors<V>(p, q, [&](auto nv, auto block) {
+        norm_rows_forward_kernel<T, V, decltype(nv)::value, decltype(block)::value><<<dim3(q.slices, q.blocks), kThreads, 0, st>>>(p, q);
+      });
+    } else {
+      const BlockPlan q = block_plan(p, v);
+      const BlockSpace s(p, q, false);
+      const long long grid = p.N * q.chunks * q.tiles;
+      if (grid > 0x7fffffffLL) {
+        e = cudaErrorInvalidConfiguration;
+        return;
+      }
+      norm_sums_kernel<T, V><<<unsigned(grid), kThreads, kThreads * V * 8, st>>>(p, q, s.seg, s.rows_of);
+      norm_apply_kernel<T, V><<<unsigned(grid), kThreads, (q.width + 1) * 8, st>>>(p, q, s.seg, s.rows_of);
+    }
+  });
+  return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 cudaError_t launch_norm_backward(const NormParams& p, cudaStream_t st) {
-  by_dtype(p.dtype, [&](auto t) {
-    norm_backward_kernel<decltype(t)><<<unsigned(p.N * p.G), kThreads, 0, st>>>(p);
-    if (p.dw || p.db) norm_weight_kernel<decltype(t)><<<p.C, kThreads, 0, st>>>(p);
+  const int v = vector_of(p);
+  cudaError_t e = cudaSuccess;
+  by_type(p.dtype, v, [&](auto t, auto vec) {
+    using T = decltype(t);
+    constexpr int V = decltype(vec)::value;
+    if (rows_form(p, v)) {
+      const RowPlan q = row_plan(p, v, kRowBlocksBackward);
+      const int shared = (q.rpi - 1) * q.gs * (p.C / p.G) * 8;
+      by_vectors<V>(p, q, [&](auto nv, auto block) {
+        auto kernel = norm_rows_backward_kernel<T, V, decltype(nv)::value, decltype(block)::value>;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, shared);
+        if (e == cudaSuccess) kernel<<<dim3(q.slices, q.blocks), kThreads, shared, st>>>(p, q);
+      });
+      if (e == cudaSuccess) launch_weights(p, static_cast<const float*>(p.workspace), q.blocks, st);
+    } else {
+      const BlockPlan q = block_plan(p, v);
+      const BlockSpace s(p, q, true);
+      const long long grid = p.N * q.chunks * q.tiles, parts = p.N * q.chunks;
+      if (grid > 0x7fffffffLL) {
+        e = cudaErrorInvalidConfiguration;
+        return;
+      }
+      norm_grad_sums_kernel<T, V><<<unsigned(grid), kThreads, kThreads * V * 8, st>>>(p, q, s.chan, s.seg, s.rows_of);
+      norm_grad_apply_kernel<T, V><<<unsigned(grid), kThreads, (q.width + 1) * 8, st>>>(p, q, s.seg, s.rows_of);
+      launch_weights(p, s.chan, static_cast<int>(parts), st);
+    }
   });
-  return cudaGetLastError();
+  return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 }  // namespace msgla

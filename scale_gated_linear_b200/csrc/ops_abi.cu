@@ -291,7 +291,7 @@ int msgla_group_norm_forward(const msgla_norm_config* cfg, long long N, long lon
   if (N * S == 0) return MSGLA_OK;
   TRY(take_f32("weight", weight, false));
   TRY(take_f32("bias", bias, false));
-  TRY(take_f32("stats", stats, false));
+  if (reinterpret_cast<uintptr_t>(stats) % 8) return set_error(MSGLA_ERR_INVALID_ARG, "stats is not 8-byte aligned");
   NormParams p = norm_params(cfg, N, S);
   Spans spans;
   TRY(take_rows("x", x, N, S, cfg->C, cfg->dtype, false, spans, &p.x));
@@ -329,7 +329,8 @@ int msgla_group_norm_backward(const msgla_norm_config* cfg, long long N, long lo
     if (dweight) TRY(copy_or_zero(dweight, nullptr, cfg->C * 4ull, st));
     return dbias ? copy_or_zero(dbias, nullptr, cfg->C * 4ull, st) : MSGLA_OK;
   }
-  TRY(take_f32("stats", stats, true));
+  if (!stats || reinterpret_cast<uintptr_t>(stats) % 8)
+    return set_error(MSGLA_ERR_INVALID_ARG, "stats is NULL or not 8-byte aligned");
   if (!gate != !dgate) return set_error(MSGLA_ERR_INVALID_ARG, "gate and dgate go together");
   NormParams p = norm_params(cfg, N, S);
   Spans spans;

@@ -78,7 +78,7 @@ def check(N, S, C, G, dtype=BF16, act="none", gated=False, mask=None, center=Tru
 @pytest.mark.parametrize("center", [True, False])
 @pytest.mark.parametrize("dtype", [BF16, F16, F32])
 @pytest.mark.parametrize("N,C,G", [(1, 8, 1), (5, 64, 4), (37, 130, 13), (3, 2048, 4), (300, 96, 3), (2, 1000, 1), (9, 33, 1),
-                                   (4, 4096, 2), (2, 6000, 1), (7, 512, 32), (2, 24, 24), (700, 520, 2)])
+                                   (4, 4096, 2), (2, 6000, 1), (7, 512, 32), (2, 24, 24), (700, 520, 2), (3, 8192, 1), (2, 9000, 1), (5, 5001, 3), (2, 5001, 1)])
 def test_rows(N, C, G, dtype, center):
     """Every row by itself: narrow and wide groups, odd widths, groups of one channel."""
     check(N, None, C, G, dtype, act="silu", gated=True, center=center, seed=C)
