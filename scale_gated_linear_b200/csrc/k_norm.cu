@@ -33,46 +33,127 @@ __device__ __forceinline__ float sigmoid(float v) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2_approx(-kLog2e * v)));
   return r;
 }
-__device__ __forceinline__ float act(int kind, float v) {
-  if (kind == kActNone) return v;
+// act(v), and with it act'(v)
+template <int KIND>
+__device__ __forceinline__ float act(float v) {
+  if (KIND == kActNone) return v;
   const float s = sigmoid(v);
-  return kind == kActSilu ? v * s : s;
+  return KIND == kActSilu ? v * s : s;
 }
-// act(v) and act'(v)
-__device__ __forceinline__ float2 act_both(int kind, float v) {
-  if (kind == kActNone) return make_float2(v, 1.f);
+template <int KIND>
+__device__ __forceinline__ float2 act_both(float v) {
+  if (KIND == kActNone) return make_float2(v, 1.f);
   const float s = sigmoid(v);
-  if (kind == kActSilu) return make_float2(v * s, s * (1.f + v * (1.f - s)));
+  if (KIND == kActSilu) return make_float2(v * s, fmaf(v * s, 1.f - s, s));
   return make_float2(s, s * (1.f - s));
 }
+// f(activation, gated) with the values as compile-time constants: one branch for a row or a
+// block's rows in place of one an element.
+template <int N>
+struct Const {
+  __host__ __device__ constexpr operator int() const { return N; }
+};
+template <typename F>
+__device__ __forceinline__ void by_act(int kind, bool gated, F&& f) {
+  auto with = [&](auto k) {
+    if (gated) f(k, Const<1>{});
+    else f(k, Const<0>{});
+  };
+  if (kind == kActNone) with(Const<kActNone>{});
+  else if (kind == kActSilu) with(Const<kActSilu>{});
+  else with(Const<kActSigmoid>{});
+}
 
-// V neighbouring channels: 16 bytes, or one element where rows are not aligned to 16.
+// V neighbouring channels as loaded: 16 bytes, or one element where rows are not aligned to 16.
 template <typename T, int V>
 struct Vec {
-  T v[V];
+  uint32_t w[V == 1 ? 1 : 4];
 };
-template <typename T, int V>
-__device__ __forceinline__ Vec<T, V> load(const T* p) {
-  Vec<T, V> r;
-  if constexpr (V == 1) {
-    r.v[0] = *p;
-  } else {
-    static_assert(V * sizeof(T) == 16, "16 bytes");
-    *reinterpret_cast<uint4*>(&r) = __ldg(reinterpret_cast<const uint4*>(p));
-  }
-  return r;
-}
 template <typename T, int V>
 __device__ __forceinline__ Vec<T, V> zeros() {
   Vec<T, V> r;
 #pragma unroll
-  for (int i = 0; i < V; ++i) r.v[i] = from_f32<T>(0.f);
+  for (uint32_t& w : r.w) w = 0;
+  return r;
+}
+template <typename T, int V>
+__device__ __forceinline__ Vec<T, V> load(const T* p) {
+  Vec<T, V> r;
+  if constexpr (V == 1) {
+    if constexpr (sizeof(T) == 4) r.w[0] = *reinterpret_cast<const uint32_t*>(p);
+    else r.w[0] = *reinterpret_cast<const uint16_t*>(p);
+  } else {
+    static_assert(V * sizeof(T) == 16, "16 bytes");
+    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
+    r.w[0] = u.x, r.w[1] = u.y, r.w[2] = u.z, r.w[3] = u.w;
+  }
   return r;
 }
 template <typename T, int V>
 __device__ __forceinline__ void store(T* p, const Vec<T, V>& r) {
-  if constexpr (V == 1) *p = r.v[0];
-  else *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(&r);
+  if constexpr (V == 1) {
+    if constexpr (sizeof(T) == 4) *reinterpret_cast<uint32_t*>(p) = r.w[0];
+    else *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(r.w[0]);
+  } else {
+    *reinterpret_cast<uint4*>(p) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+  }
+}
+// The two 16-bit values of a word as f32, and back.
+template <typename T>
+__device__ __forceinline__ float2 pair_f32(uint32_t w) {
+  if constexpr (std::is_same_v<T, __half>) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  else return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pair_round(float a, float b) {
+  if constexpr (std::is_same_v<T, __half>) return pack_half2(a, b);
+  else return pack_bf162(a, b);
+}
+template <typename T, int V>
+__device__ __forceinline__ void unpack(const Vec<T, V>& r, float (&f)[V]) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) f[e] = __uint_as_float(r.w[e]);
+  } else if constexpr (V == 1) {
+    f[0] = pair_f32<T>(r.w[0]).x;
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; e += 2) {
+      const float2 v = pair_f32<T>(r.w[e / 2]);
+      f[e] = v.x, f[e + 1] = v.y;
+    }
+  }
+}
+template <typename T, int V>
+__device__ __forceinline__ Vec<T, V> pack(const float (&f)[V]) {
+  Vec<T, V> r;
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) r.w[e] = __float_as_uint(f[e]);
+  } else if constexpr (V == 1) {
+    r.w[0] = pair_round<T>(f[0], 0.f);
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; e += 2) r.w[e / 2] = pair_round<T>(f[e], f[e + 1]);
+  }
+  return r;
+}
+
+// V weights from channel c on (16-byte loads where V allows), or `none` without weights
+template <int V>
+__device__ __forceinline__ void weights(const float* w, int c, bool in, float none, float (&to)[V]) {
+  if (!w || !in) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) to[e] = none;
+  } else if constexpr (V == 1) {
+    to[0] = __ldg(w + c);
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; e += 4) {
+      const float4 f = __ldg(reinterpret_cast<const float4*>(w + c + e));
+      to[e] = f.x, to[e + 1] = f.y, to[e + 2] = f.z, to[e + 3] = f.w;
+    }
+  }
 }
 template <typename T>
 __device__ __forceinline__ T* at(const Rows& r, long long n, long long s, int c) {
@@ -83,32 +164,42 @@ __device__ __forceinline__ float team_sum(float v, int team) {
   for (int o = team >> 1; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
   return v;
 }
-// Two sums over a team, or with BLOCK over the whole block (`part`: its warps' sums, two
-// buffers taken in turn so that one barrier a call is enough).
-template <bool BLOCK>
-__device__ __forceinline__ float2 sums_of(float a, float b, int team, float2 (*part)[kThreads / 32], int turn) {
-  a = team_sum(a, BLOCK ? 32 : team);
-  b = team_sum(b, BLOCK ? 32 : team);
-  if constexpr (BLOCK) {
-    if (lane_id() == 0) part[turn][warp_id()] = make_float2(a, b);
-    __syncthreads();
-    a = b = 0.f;
+// N sums over a team of TEAM threads (0: `team`, below 32). A whole block's go through `part`,
+// two buffers taken in turn so that one barrier a call is enough.
+template <int TEAM, int N>
+__device__ __forceinline__ void sums_of(float (&v)[N], int team, float (*part)[2][kThreads / 32], int turn) {
+  if constexpr (TEAM == 0) {
+    for (int o = team >> 1; o; o >>= 1)
 #pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) {
-      a += part[turn][i].x;
-      b += part[turn][i].y;
+      for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(~0u, v[k], o);
+  } else {
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+#pragma unroll
+      for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(~0u, v[k], o);
+  }
+  if constexpr (TEAM == kThreads) {
+    if (lane_id() == 0)
+#pragma unroll
+      for (int k = 0; k < N; ++k) part[turn][k][warp_id()] = v[k];
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      v[k] = 0.f;
+#pragma unroll
+      for (int i = 0; i < kThreads / 32; ++i) v[k] += part[turn][k][i];
     }
   }
-  return make_float2(a, b);
 }
 
 // Gradient of the value before the activation, and of the gate.
-__device__ __forceinline__ float grad_v(const NormParams& p, float v, float dy, float gate, float& dgate) {
-  if (!p.gate.ptr) {
+template <int KIND, bool GATED>
+__device__ __forceinline__ float grad_v(float v, float dy, float gate, float& dgate) {
+  if (!GATED) {
     dgate = 0.f;
-    return dy * act_both(p.act, v).y;
+    return dy * act_both<KIND>(v).y;
   }
-  const float2 a = act_both(p.act, gate);
+  const float2 a = act_both<KIND>(gate);
   dgate = dy * v * a.y;
   return dy * a.x;
 }
@@ -121,134 +212,143 @@ struct RowPlan {
 
 template <typename T, int V, int NV>
 struct RowLane {
-  int c[NV];    // channels
-  bool in[NV];  // whether they exist
+  int c, step;  // first channel, channels between two vectors
   int g, row;   // group, and the first row
-  bool active;
+  int vectors;  // how many of the NV exist
   __device__ __forceinline__ RowLane(const NormParams& p, const RowPlan& q) {
     const int team = threadIdx.x / q.team, tl = threadIdx.x % q.team, cg = p.C / p.G;
     g = blockIdx.x * q.gs + team % q.gs;
     row = team / q.gs;
-    active = row < q.rpi && g < p.G;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int o = (i * q.team + tl) * V;
-      in[i] = active && o < cg;
-      c[i] = g * cg + o;
-    }
+    step = q.team * V;
+    c = g * cg + tl * V;
+    vectors = row < q.rpi && g < p.G && tl * V < cg ? (cg - tl * V + step - 1) / step : 0;
+  }
+  __device__ __forceinline__ bool in(int i) const { return i < vectors; }
+};
+// A lane's vectors of the rows it takes one after another.
+template <typename T, int V>
+struct RowPtr {
+  T* at;
+  long long step;
+  __device__ __forceinline__ RowPtr(const Rows& r, long long row, long long rows, int c) {
+    at = r.ptr ? static_cast<T*>(r.ptr) + row * r.batch + c : nullptr;
+    step = rows * r.batch;
   }
 };
 
-template <typename T, int V, int NV, bool BLOCK>
-__global__ void __launch_bounds__(kThreads) norm_rows_forward_kernel(const NormParams p, const RowPlan q) {
-  __shared__ float2 part[2][kThreads / 32];
-  constexpr bool kKeep = V * NV <= 16;  // weights in registers
+template <typename T, int V, int NV, int TEAM>
+__global__ void __launch_bounds__(kThreads, V * NV <= 16 ? 3 : 1) norm_rows_forward_kernel(const NormParams p, const RowPlan q) {
+  __shared__ float part[2][2][kThreads / 32];
   const RowLane<T, V, NV> l(p, q);
   const float inv = 1.f / (p.C / p.G);
   const bool gated = p.gate.ptr;
-  float w[kKeep ? NV : 1][V], b[kKeep ? NV : 1][V];
-  auto weights = [&](int i, float (&wi)[V], float (&bi)[V]) {
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      wi[e] = p.w && l.in[i] ? __ldg(p.w + l.c[i] + e) : 1.f;
-      bi[e] = p.b && l.in[i] ? __ldg(p.b + l.c[i] + e) : 0.f;
-    }
-  };
-  if constexpr (kKeep) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) weights(i, w[i], b[i]);
-  }
   const long long step = static_cast<long long>(gridDim.y) * q.rpi;
+  long long base = static_cast<long long>(blockIdx.y) * q.rpi, row = base + l.row;
+  RowPtr<T, V> px(p.x, row, step, l.c), pg(p.gate, row, step, l.c), py(p.y, row, step, l.c);
   Vec<T, V> xn[NV], gn[NV];
   bool valid_next;
-  auto fetch = [&](long long row) {
-    valid_next = l.active && row < p.N && (!p.mask || p.mask[row]);
+  auto fetch = [&](long long r) {
+    valid_next = r < p.N && (!p.mask || p.mask[r]);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      xn[i] = valid_next && l.in[i] ? load<T, V>(at<T>(p.x, row, 0, l.c[i])) : zeros<T, V>();
-      gn[i] = valid_next && l.in[i] && gated ? load<T, V>(at<T>(p.gate, row, 0, l.c[i])) : zeros<T, V>();
+      xn[i] = valid_next && l.in(i) ? load<T, V>(px.at + i * l.step) : zeros<T, V>();
+      gn[i] = valid_next && l.in(i) && gated ? load<T, V>(pg.at + i * l.step) : zeros<T, V>();
     }
+    px.at += px.step;
+    pg.at += pg.step;
   };
-  long long row = static_cast<long long>(blockIdx.y) * q.rpi + l.row;
   fetch(row);
-  for (long long base = static_cast<long long>(blockIdx.y) * q.rpi; base < p.N; base += step, row += step) {
-    float x[NV][V];
+  for (; base < p.N; base += step, row += step, py.at += py.step) {
+    float x[NV][V], sum[1] = {0.f}, ss[1] = {0.f};
     Vec<T, V> gt[NV];
     const bool valid = valid_next;
-    float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       gt[i] = gn[i];
+      unpack(xn[i], x[i]);
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        x[i][e] = to_f32(xn[i].v[e]);
-        sum += x[i][e];
-      }
+      for (int e = 0; e < V; ++e) sum[0] += x[i][e];
     }
     if (base + step < p.N) fetch(row + step);
-    const float mean = p.center ? sums_of<BLOCK>(sum, 0.f, q.team, part, 0).x * inv : 0.f;
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        x[i][e] = l.in[i] ? x[i][e] - mean : 0.f;
-        ss = fmaf(x[i][e], x[i][e], ss);
-      }
-    const float rstd = 1.f / sqrtf(sums_of<BLOCK>(ss, 0.f, q.team, part, 1).x * inv + p.eps);
-    if (BLOCK && !p.center) __syncthreads();  // the next row writes the same buffer
-    if (!l.active || row >= p.N) continue;
-    if (p.stats && threadIdx.x % q.team == 0)
-      *reinterpret_cast<float2*>(p.stats + 2 * (row * p.G + l.g)) = make_float2(mean, rstd);
+    if (p.center) sums_of<TEAM>(sum, q.team, part, 0);
+    const float mean = p.center ? sum[0] * inv : 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if (!l.in[i]) continue;
-      float wl[V], bl[V];
-      if constexpr (!kKeep) weights(i, wl, bl);
-      Vec<T, V> y;
+      const float off = l.in(i) ? mean : 0.f;  // what does not exist stays zero
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        const float v = fmaf(x[i][e] * rstd, kKeep ? w[kKeep ? i : 0][e] : wl[e], kKeep ? b[kKeep ? i : 0][e] : bl[e]);
-        const float r = gated ? v * act(p.act, to_f32(gt[i].v[e])) : act(p.act, v);
-        y.v[e] = from_f32<T>(valid ? r : 0.f);
+        x[i][e] -= off;
+        ss[0] = fmaf(x[i][e], x[i][e], ss[0]);
       }
-      store<T, V>(at<T>(p.y, row, 0, l.c[i]), y);
     }
+    sums_of<TEAM>(ss, q.team, part, 1);
+    const float rstd = 1.f / sqrtf(ss[0] * inv + p.eps);
+    if (TEAM == kThreads && !p.center) __syncthreads();  // the next row writes the same buffer
+    if (row >= p.N) continue;
+    if (p.stats && l.vectors && threadIdx.x % q.team == 0)
+      *reinterpret_cast<float2*>(p.stats + 2 * (row * p.G + l.g)) = make_float2(mean, rstd);
+    if (!valid) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (l.in(i)) store<T, V>(py.at + i * l.step, zeros<T, V>());
+      continue;
+    }
+    by_act(p.act, gated, [&](auto kind, auto with_gate) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        if (!l.in(i)) continue;
+        float w[V], b[V], g[V], y[V];
+        weights<V>(p.w, l.c + i * l.step, true, 1.f, w);
+        weights<V>(p.b, l.c + i * l.step, true, 0.f, b);
+        if (with_gate) unpack(gt[i], g);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const float v = fmaf(x[i][e] * rstd, w[e], b[e]);
+          y[e] = with_gate ? v * act<kind>(g[e]) : act<kind>(v);
+        }
+        store<T, V>(py.at + i * l.step, pack<T, V>(y));
+      }
+    });
   }
 }
 
 // Weight gradients: partial sums [blocks][2][C] (dw, db) in the workspace.
-template <typename T, int V, int NV, bool BLOCK>
-__global__ void __launch_bounds__(kThreads) norm_rows_backward_kernel(const NormParams p, const RowPlan q) {
-  __shared__ float2 part[2][kThreads / 32];
-  int turn = 0;
+template <typename T, int V, int NV, int TEAM>
+__global__ void __launch_bounds__(kThreads, V * NV <= 16 ? 2 : 1) norm_rows_backward_kernel(const NormParams p, const RowPlan q) {
+  __shared__ float part[2][2][kThreads / 32];
   extern __shared__ float shared[];  // [rpi - 1][gs * cg][2]
+  int turn = 0;
   const RowLane<T, V, NV> l(p, q);
   const int cg = p.C / p.G;
   const float inv = 1.f / cg;
   const bool gated = p.gate.ptr;
   float dw[NV][V] = {}, db[NV][V] = {};
   const long long step = static_cast<long long>(gridDim.y) * q.rpi;
+  long long base = static_cast<long long>(blockIdx.y) * q.rpi, row = base + l.row;
+  RowPtr<T, V> px(p.x, row, step, l.c), pd(p.dy, row, step, l.c), pg(p.gate, row, step, l.c), ox(p.dx, row, step, l.c),
+      og(p.dgate, row, step, l.c);
   Vec<T, V> xn[NV], dn[NV], gn[NV];
   float2 sn;
   bool valid_next;
-  auto fetch = [&](long long row) {
-    valid_next = l.active && row < p.N && (!p.mask || p.mask[row]);
-    sn = valid_next ? *reinterpret_cast<const float2*>(p.stats + 2 * (row * p.G + l.g)) : make_float2(0.f, 0.f);
+  auto fetch = [&](long long r) {
+    valid_next = r < p.N && l.vectors && (!p.mask || p.mask[r]);
+    sn = valid_next ? *reinterpret_cast<const float2*>(p.stats + 2 * (r * p.G + l.g)) : make_float2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const bool in = valid_next && l.in[i];
-      xn[i] = in ? load<T, V>(at<T>(p.x, row, 0, l.c[i])) : zeros<T, V>();
-      dn[i] = in ? load<T, V>(at<T>(p.dy, row, 0, l.c[i])) : zeros<T, V>();
-      gn[i] = in && gated ? load<T, V>(at<T>(p.gate, row, 0, l.c[i])) : zeros<T, V>();
+      const bool in = valid_next && l.in(i);
+      xn[i] = in ? load<T, V>(px.at + i * l.step) : zeros<T, V>();
+      dn[i] = in ? load<T, V>(pd.at + i * l.step) : zeros<T, V>();
+      gn[i] = in && gated ? load<T, V>(pg.at + i * l.step) : zeros<T, V>();
     }
+    px.at += px.step;
+    pd.at += pd.step;
+    pg.at += pg.step;
   };
-  long long row = static_cast<long long>(blockIdx.y) * q.rpi + l.row;
   fetch(row);
-  for (long long base = static_cast<long long>(blockIdx.y) * q.rpi; base < p.N; base += step, row += step) {
+  for (; base < p.N; base += step, row += step, ox.at += ox.step, og.at += og.step) {
     Vec<T, V> x[NV], d[NV], gt[NV];
     const float2 st = sn;
-    const bool valid = valid_next, here = l.active && row < p.N;
+    const bool valid = valid_next, here = row < p.N;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       x[i] = xn[i];
@@ -256,63 +356,71 @@ __global__ void __launch_bounds__(kThreads) norm_rows_backward_kernel(const Norm
       gt[i] = gn[i];
     }
     if (base + step < p.N) fetch(row + step);
-    float s1 = 0.f, s2 = 0.f, xh[NV][V], dv[NV][V];
+    float s[2] = {0.f, 0.f}, dv[NV][V];
+    by_act(p.act, gated, [&](auto kind, auto with_gate) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        float w[V], b[V], xv[V], dy[V], gv[V], dg[V];
+        weights<V>(p.w, l.c + i * l.step, l.in(i), 1.f, w);
+        weights<V>(p.b, l.c + i * l.step, l.in(i), 0.f, b);
+        unpack(x[i], xv);
+        unpack(d[i], dy);
+        if (with_gate) unpack(gt[i], gv);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {  // where nothing was loaded dy = 0, and with it every sum's part
+          const float xh = (xv[e] - st.x) * st.y;
+          const float t = grad_v<kind, with_gate>(fmaf(xh, w[e], b[e]), dy[e], with_gate ? gv[e] : 0.f, dg[e]);
+          dw[i][e] = fmaf(t, xh, dw[i][e]);
+          db[i][e] += t;
+          dv[i][e] = t * w[e];
+          s[0] += dv[i][e];
+          s[1] = fmaf(dv[i][e], xh, s[1]);
+        }
+        if (with_gate && here && l.in(i)) store<T, V>(og.at + i * l.step, pack<T, V>(dg));
+      }
+    });
+    sums_of<TEAM>(s, q.team, part, turn ^= 1);
+    const float m1 = p.center ? s[0] * inv : 0.f, m2 = s[1] * inv;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      Vec<T, V> dg;
+      float xv[V], dx[V];
+      unpack(x[i], xv);
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        const bool in = valid && l.in[i];
-        const float w = p.w && l.in[i] ? __ldg(p.w + l.c[i] + e) : 1.f, b = p.b && l.in[i] ? __ldg(p.b + l.c[i] + e) : 0.f;
-        xh[i][e] = in ? (to_f32(x[i].v[e]) - st.x) * st.y : 0.f;
-        float g;
-        const float t = in ? grad_v(p, fmaf(xh[i][e], w, b), to_f32(d[i].v[e]), to_f32(gt[i].v[e]), g) : g = 0.f;
-        dg.v[e] = from_f32<T>(g);
-        dw[i][e] = fmaf(t, xh[i][e], dw[i][e]);
-        db[i][e] += t;
-        dv[i][e] = t * w;
-        s1 += dv[i][e];
-        s2 = fmaf(dv[i][e], xh[i][e], s2);
+        const float xh = (xv[e] - st.x) * st.y;
+        dx[e] = (dv[i][e] - m1 - xh * m2) * st.y;
       }
-      if (gated && here && l.in[i]) store<T, V>(at<T>(p.dgate, row, 0, l.c[i]), dg);
-    }
-    const float2 sums = sums_of<BLOCK>(s1, s2, q.team, part, turn ^= 1);
-    const float m1 = p.center ? sums.x * inv : 0.f, m2 = sums.y * inv;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      Vec<T, V> dx;
-#pragma unroll
-      for (int e = 0; e < V; ++e) dx.v[e] = from_f32<T>(valid ? (dv[i][e] - m1 - xh[i][e] * m2) * st.y : 0.f);
-      if (here && l.in[i]) store<T, V>(at<T>(p.dx, row, 0, l.c[i]), dx);
+      if (here && l.in(i)) store<T, V>(ox.at + i * l.step, valid ? pack<T, V>(dx) : zeros<T, V>());
     }
   }
   if (!p.dw && !p.db) return;
   // the block's rows of every channel, summed in order by the first one's team
   const int width = q.gs * cg, c0 = blockIdx.x * width;
-  if (l.active && l.row > 0) {
+  if (l.row > 0) {
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      if (l.in[i])
+      if (l.in(i))
 #pragma unroll
         for (int e = 0; e < V; ++e)
-          *reinterpret_cast<float2*>(shared + 2 * ((l.row - 1) * width + l.c[i] + e - c0)) = make_float2(dw[i][e], db[i][e]);
+          *reinterpret_cast<float2*>(shared + 2 * ((l.row - 1) * width + l.c + i * l.step + e - c0)) = make_float2(dw[i][e], db[i][e]);
   }
   __syncthreads();
-  if (!l.active || l.row > 0) return;
+  if (l.row > 0) return;
   float* out = static_cast<float*>(p.workspace) + static_cast<size_t>(blockIdx.y) * 2 * p.C;
 #pragma unroll
   for (int i = 0; i < NV; ++i)
-    if (l.in[i])
+    if (l.in(i))
 #pragma unroll
       for (int e = 0; e < V; ++e) {
+        const int c = l.c + i * l.step + e;
         float2 s = make_float2(dw[i][e], db[i][e]);
         for (int r = 1; r < q.rpi; ++r) {
-          const float2 o = *reinterpret_cast<const float2*>(shared + 2 * ((r - 1) * width + l.c[i] + e - c0));
+          const float2 o = *reinterpret_cast<const float2*>(shared + 2 * ((r - 1) * width + c - c0));
           s.x += o.x;
           s.y += o.y;
         }
-        out[l.c[i] + e] = s.x;
-        out[p.C + l.c[i] + e] = s.y;
+        out[c] = s.x;
+        out[p.C + c] = s.y;
       }
 }
 
@@ -363,39 +471,67 @@ struct Part {
   }
 };
 
+constexpr int kUnroll = 4;  // rows a thread has on their way at once
+// Valid rows among s, s + ty, .. s + 3 ty (bit k: the k-th).
+__device__ __forceinline__ uint32_t rows_valid(const uint8_t* m, long long s, long long s1, int ty) {
+  uint32_t bits = 0;
+#pragma unroll
+  for (int k = 0; k < kUnroll; ++k)
+    if (s + k * ty < s1 && (!m || m[s + k * ty])) bits |= 1u << k;
+  return bits;
+}
+
 // Forward sums: float2 (mean, sum of squared differences) per segment at
 // seg[(n * chunks + chunk) * C + channel]; the valid rows of each (n, chunk) at rows_of.
 template <typename T, int V>
 __global__ void __launch_bounds__(kThreads) norm_sums_kernel(const NormParams p, const BlockPlan q, float2* seg, float* rows_of) {
-  extern __shared__ float2 cell[];  // [ty][width]
+  __shared__ float2 cell[kThreads];  // a thread's V channels: mean and squares
   __shared__ int counts[kThreads];
   const Part part(q);
   const int tx = threadIdx.x % q.tx, ty = threadIdx.x / q.tx, c = part.tile * q.width + tx * V, cg = p.C / p.G;
   const long long s0 = static_cast<long long>(part.chunk) * q.rows, s1 = min(s0 + q.rows, p.S);
   const uint8_t* m = p.mask ? p.mask + part.n * p.S : nullptr;
-  float first[V] = {}, sum[V] = {}, sq[V] = {};
+  float first = 0.f, sum[V] = {}, sq[V] = {};
   int count = 0;
-  if (c < p.C)
-    for (long long s = s0 + ty; s < s1; s += q.ty) {
-      if (m && !m[s]) continue;
-      const Vec<T, V> x = load<T, V>(at<T>(p.x, part.n, s, c));
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float v = to_f32(x.v[e]);
-        if (count == 0) first[e] = p.center ? v : 0.f;
-        const float d = v - first[e];
-        sum[e] += d;
-        sq[e] = fmaf(d, d, sq[e]);
-      }
-      ++count;
+  if (c < p.C) {
+    const T* x = at<T>(p.x, part.n, 0, c);
+    long long s = s0 + ty;
+    if (p.center) {  // differences from the thread's first value
+      while (s < s1 && m && !m[s]) s += q.ty;
+      if (s < s1) first = to_f32(x[s * p.x.row]);
     }
-  const float n = static_cast<float>(max(count, 1));
+    for (; s < s1; s += kUnroll * q.ty) {
+      const uint32_t bits = rows_valid(m, s, s1, q.ty);
+      Vec<T, V> v[kUnroll];
 #pragma unroll
-  for (int e = 0; e < V; ++e)
-    if (c < p.C) {
-      const float mean = sum[e] / n;
-      cell[ty * q.width + tx * V + e] = make_float2(p.center ? first[e] + mean : 0.f, p.center ? fmaxf(sq[e] - sum[e] * mean, 0.f) : sq[e]);
+      for (int k = 0; k < kUnroll; ++k)
+        if (bits >> k & 1) v[k] = load<T, V>(x + (s + k * q.ty) * p.x.row);
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k)
+        if (bits >> k & 1) {
+          float f[V];
+          unpack(v[k], f);
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            const float d = f[e] - first;
+            sum[e] += d;
+            sq[e] = fmaf(d, d, sq[e]);
+          }
+        }
+      count += __popc(bits);
     }
+  }
+  // the V channels are of one group: about their common mean
+  float total = 0.f, squares = 0.f;
+#pragma unroll
+  for (int e = 0; e < V; ++e) total += sum[e];
+  const float n = static_cast<float>(max(count, 1)), off = p.center ? total / (n * V) : 0.f;
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    const float own = sum[e] / n;  // sum (d - off)^2 = sum (d - own)^2 + n (own - off)^2
+    squares += p.center ? fmaxf(sq[e] - sum[e] * own, 0.f) + n * (own - off) * (own - off) : sq[e];
+  }
+  cell[threadIdx.x] = make_float2(first + off, squares);
   if (tx == 0) counts[ty] = count;
   __syncthreads();
   int rows = 0;
@@ -404,27 +540,27 @@ __global__ void __launch_bounds__(kThreads) norm_sums_kernel(const NormParams p,
   // one warp joins a segment: its mean, then the squares about it
   const int t0 = part.tile * q.width, t1 = min(t0 + q.width, p.C);
   for (int g = t0 / cg + warp_id(); g * cg < t1; g += kThreads / 32) {
-    const int a = max(g * cg, t0), wide = min((g + 1) * cg, t1) - a, cells = wide * q.ty;
-    float total = 0.f, squares = 0.f, base = 0.f, mean = 0.f;
+    const int a = max(g * cg, t0), x0 = (a - t0) / V, wide = (min((g + 1) * cg, t1) - a) / V, cells = wide * q.ty;
+    float sums = 0.f, sqs = 0.f, mean = 0.f;
     if (p.center && rows) {
       int r0 = 0;
       while (counts[r0] == 0) ++r0;
-      base = cell[r0 * q.width + a - t0].x;
+      const float base = cell[r0 * q.tx + x0].x;
       for (int i = lane_id(); i < cells; i += 32) {
         const int r = i / wide;
-        if (counts[r]) total += counts[r] * (cell[r * q.width + a - t0 + i % wide].x - base);
+        if (counts[r]) sums += counts[r] * (cell[r * q.tx + x0 + i - r * wide].x - base);
       }
-      mean = base + team_sum(total, 32) / (static_cast<float>(rows) * wide);
+      mean = base + team_sum(sums, 32) / (static_cast<float>(rows) * wide);
     }
     for (int i = lane_id(); i < cells; i += 32) {
       const int r = i / wide;
       if (!counts[r]) continue;
-      const float2 v = cell[r * q.width + a - t0 + i % wide];
+      const float2 v = cell[r * q.tx + x0 + i - r * wide];
       const float d = v.x - mean;
-      squares += v.y + counts[r] * d * d;
+      sqs += v.y + counts[r] * V * d * d;
     }
-    squares = team_sum(squares, 32);
-    if (lane_id() == 0) seg[(part.n * q.chunks + part.chunk) * p.C + a] = make_float2(mean, squares);
+    sqs = team_sum(sqs, 32);
+    if (lane_id() == 0) seg[(part.n * q.chunks + part.chunk) * p.C + a] = make_float2(mean, sqs);
   }
 }
 
@@ -490,19 +626,37 @@ __global__ void __launch_bounds__(kThreads) norm_apply_kernel(const NormParams p
   }
   const long long s0 = static_cast<long long>(part.chunk) * q.rows, s1 = min(s0 + q.rows, p.S);
   const uint8_t* m = p.mask ? p.mask + part.n * p.S : nullptr;
-  for (long long s = s0 + ty; s < s1; s += q.ty) {
-    Vec<T, V> y = zeros<T, V>();
-    if (!m || m[s]) {
-      const Vec<T, V> x = load<T, V>(at<T>(p.x, part.n, s, c));
-      const Vec<T, V> gt = p.gate.ptr ? load<T, V>(at<T>(p.gate, part.n, s, c)) : x;
+  const T* xp = at<T>(p.x, part.n, 0, c);
+  const T* gp = at<T>(p.gate, part.n, 0, c);
+  T* yp = at<T>(p.y, part.n, 0, c);
+  by_act(p.act, p.gate.ptr, [&](auto kind, auto gated) {
+    for (long long s = s0 + ty; s < s1; s += kUnroll * q.ty) {
+      const uint32_t bits = rows_valid(m, s, s1, q.ty);
+      Vec<T, V> x[kUnroll], gt[kUnroll];
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float v = fmaf(to_f32(x.v[e]) - mean[e], w[e], b[e]);
-        y.v[e] = from_f32<T>(p.gate.ptr ? v * act(p.act, to_f32(gt.v[e])) : act(p.act, v));
+      for (int k = 0; k < kUnroll; ++k)
+        if (bits >> k & 1) {
+          x[k] = load<T, V>(xp + (s + k * q.ty) * p.x.row);
+          if (gated) gt[k] = load<T, V>(gp + (s + k * q.ty) * p.gate.row);
+        }
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) {
+        Vec<T, V> y = zeros<T, V>();
+        if (bits >> k & 1) {
+          float xv[V], gv[V], r[V];
+          unpack(x[k], xv);
+          if (gated) unpack(gt[k], gv);
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            const float v = fmaf(xv[e] - mean[e], w[e], b[e]);
+            r[e] = gated ? v * act<kind>(gv[e]) : act<kind>(v);
+          }
+          y = pack<T, V>(r);
+        }
+        if (s + k * q.ty < s1) store<T, V>(yp + (s + k * q.ty) * p.y.row, y);
       }
     }
-    store<T, V>(at<T>(p.y, part.n, s, c), y);
-  }
+  });
 }
 
 // Backward sums: per channel dw and db of every (n, chunk) as chan[(n * chunks + chunk)][2][C], per
@@ -528,20 +682,38 @@ __global__ void __launch_bounds__(kThreads) norm_grad_sums_kernel(const NormPara
       w[e] = p.w ? p.w[c + e] : 1.f;
       b[e] = p.b ? p.b[c + e] : 0.f;
     }
-    for (long long s = s0 + ty; s < s1; s += q.ty) {
-      if (m && !m[s]) continue;
-      ++count;
-      const Vec<T, V> x = load<T, V>(at<T>(p.x, part.n, s, c)), d = load<T, V>(at<T>(p.dy, part.n, s, c));
-      const Vec<T, V> gt = p.gate.ptr ? load<T, V>(at<T>(p.gate, part.n, s, c)) : x;
+    const T* xp = at<T>(p.x, part.n, 0, c);
+    const T* dp = at<T>(p.dy, part.n, 0, c);
+    const T* gp = at<T>(p.gate, part.n, 0, c);
+    by_act(p.act, p.gate.ptr, [&](auto kind, auto gated) {
+      for (long long s = s0 + ty; s < s1; s += kUnroll * q.ty) {
+        const uint32_t bits = rows_valid(m, s, s1, q.ty);
+        count += __popc(bits);
+        Vec<T, V> x[kUnroll], d[kUnroll], gt[kUnroll];
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float xh = (to_f32(x.v[e]) - mean[e]) * rstd[e];
-        float dg;
-        const float t = grad_v(p, fmaf(xh, w[e], b[e]), to_f32(d.v[e]), to_f32(gt.v[e]), dg);
-        dw[e] = fmaf(t, xh, dw[e]);
-        db[e] += t;
+        for (int k = 0; k < kUnroll; ++k)
+          if (bits >> k & 1) {
+            x[k] = load<T, V>(xp + (s + k * q.ty) * p.x.row);
+            d[k] = load<T, V>(dp + (s + k * q.ty) * p.dy.row);
+            if (gated) gt[k] = load<T, V>(gp + (s + k * q.ty) * p.gate.row);
+          }
+#pragma unroll
+        for (int k = 0; k < kUnroll; ++k)
+          if (bits >> k & 1) {
+            float xv[V], dy[V], gv[V], dg;
+            unpack(x[k], xv);
+            unpack(d[k], dy);
+            if (gated) unpack(gt[k], gv);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+              const float xh = (xv[e] - mean[e]) * rstd[e];
+              const float t = grad_v<kind, gated>(fmaf(xh, w[e], b[e]), dy[e], gated ? gv[e] : 0.f, dg);
+              dw[e] = fmaf(t, xh, dw[e]);
+              db[e] += t;
+            }
+          }
       }
-    }
+    });
 #pragma unroll
     for (int e = 0; e < V; ++e) cell[ty * q.width + tx * V + e] = make_float2(dw[e], db[e]);
   }
@@ -618,23 +790,46 @@ __global__ void __launch_bounds__(kThreads) norm_grad_apply_kernel(const NormPar
   }
   const long long s0 = static_cast<long long>(part.chunk) * q.rows, s1 = min(s0 + q.rows, p.S);
   const uint8_t* m = p.mask ? p.mask + part.n * p.S : nullptr;
-  for (long long s = s0 + ty; s < s1; s += q.ty) {
-    Vec<T, V> dx = zeros<T, V>(), dgate = dx;
-    if (!m || m[s]) {
-      const Vec<T, V> x = load<T, V>(at<T>(p.x, part.n, s, c)), d = load<T, V>(at<T>(p.dy, part.n, s, c));
-      const Vec<T, V> gt = p.gate.ptr ? load<T, V>(at<T>(p.gate, part.n, s, c)) : x;
+  const T* xp = at<T>(p.x, part.n, 0, c);
+  const T* dp = at<T>(p.dy, part.n, 0, c);
+  const T* gp = at<T>(p.gate, part.n, 0, c);
+  T* ox = at<T>(p.dx, part.n, 0, c);
+  T* og = at<T>(p.dgate, part.n, 0, c);
+  by_act(p.act, p.gate.ptr, [&](auto kind, auto gated) {
+    for (long long s = s0 + ty; s < s1; s += kUnroll * q.ty) {
+      const uint32_t bits = rows_valid(m, s, s1, q.ty);
+      Vec<T, V> x[kUnroll], d[kUnroll], gt[kUnroll];
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float xh = (to_f32(x.v[e]) - mean[e]) * rstd[e];
-        float dg;
-        const float t = grad_v(p, fmaf(xh, w[e], b[e]), to_f32(d.v[e]), to_f32(gt.v[e]), dg) * w[e];
-        dx.v[e] = from_f32<T>((t - m1[e] - xh * m2[e]) * rstd[e]);
-        dgate.v[e] = from_f32<T>(dg);
+      for (int k = 0; k < kUnroll; ++k)
+        if (bits >> k & 1) {
+          x[k] = load<T, V>(xp + (s + k * q.ty) * p.x.row);
+          d[k] = load<T, V>(dp + (s + k * q.ty) * p.dy.row);
+          if (gated) gt[k] = load<T, V>(gp + (s + k * q.ty) * p.gate.row);
+        }
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) {
+        Vec<T, V> dx = zeros<T, V>(), dgate = dx;
+        if (bits >> k & 1) {
+          float xv[V], dy[V], gv[V], dg[V], r[V];
+          unpack(x[k], xv);
+          unpack(d[k], dy);
+          if (gated) unpack(gt[k], gv);
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            const float xh = (xv[e] - mean[e]) * rstd[e];
+            const float t = grad_v<kind, gated>(fmaf(xh, w[e], b[e]), dy[e], gated ? gv[e] : 0.f, dg[e]) * w[e];
+            r[e] = (t - m1[e] - xh * m2[e]) * rstd[e];
+          }
+          dx = pack<T, V>(r);
+          if (gated) dgate = pack<T, V>(dg);
+        }
+        if (s + k * q.ty < s1) {
+          store<T, V>(ox + (s + k * q.ty) * p.dx.row, dx);
+          if (gated) store<T, V>(og + (s + k * q.ty) * p.dgate.row, dgate);
+        }
       }
     }
-    store<T, V>(at<T>(p.dx, part.n, s, c), dx);
-    if (p.gate.ptr) store<T, V>(at<T>(p.dgate, part.n, s, c), dgate);
-  }
+  });
 }
 
 // ---------------------------------------------------------------- plans and launches
@@ -653,7 +848,8 @@ bool aligned16(const Rows& r, int dtype) {
 int vector_of(const NormParams& p) {
   const int run = p.dtype == kF32 ? 4 : 8;
   const bool ok = p.C / p.G % run == 0 && aligned16(p.x, p.dtype) && aligned16(p.gate, p.dtype) && aligned16(p.y, p.dtype) &&
-                  aligned16(p.dy, p.dtype) && aligned16(p.dx, p.dtype) && aligned16(p.dgate, p.dtype);
+                  aligned16(p.dy, p.dtype) && aligned16(p.dx, p.dtype) && aligned16(p.dgate, p.dtype) &&
+                  reinterpret_cast<uintptr_t>(p.w) % 16 == 0 && reinterpret_cast<uintptr_t>(p.b) % 16 == 0;
   return ok ? run : 1;
 }
 
@@ -689,7 +885,7 @@ BlockPlan block_plan(const NormParams& p, int v) {
   q.width = q.tx * v;
   q.tiles = (p.C + q.width - 1) / q.width;
   const long long blocks = p.N * q.tiles, rows_at_once = (p.S + q.ty - 1) / q.ty;
-  long long chunks = (8LL * multiprocessors() + blocks - 1) / blocks;
+  long long chunks = (4LL * multiprocessors() + blocks - 1) / blocks;
   const long long least = (rows_at_once + 63) / 64, most = rows_at_once < 512 ? rows_at_once : 512;
   if (chunks < least) chunks = least;
   if (chunks > most) chunks = most;
@@ -726,15 +922,16 @@ void by_type(int dtype, int v, F&& f) {
   else if (dtype == kF16) by_vec(__half{});
   else by_vec(float{});
 }
-// f(vectors a lane, BLOCK) for the smallest number that holds a group
+// f(vectors a lane, TEAM) for the smallest number that holds a group
 template <int V, typename F>
 void by_vectors(const NormParams& p, const RowPlan& q, F&& f) {
   const int need = (p.C / p.G + q.team * V - 1) / (q.team * V);
   auto with = [&](auto nv) {
-    if (q.team > 32) f(nv, std::true_type{});
-    else f(nv, std::false_type{});
+    if (q.team > 32) f(nv, std::integral_constant<int, kThreads>{});
+    else f(nv, std::integral_constant<int, 32>{});
   };
-  if (need <= 1) with(std::integral_constant<int, 1>{});
+  if (q.team < 32) f(std::integral_constant<int, 1>{}, std::integral_constant<int, 0>{});
+  else if (need <= 1) with(std::integral_constant<int, 1>{});
   else if (need <= 2) with(std::integral_constant<int, 2>{});
   else if (need <= 4) with(std::integral_constant<int, 4>{});
   else if constexpr (V <= 4) {
@@ -743,7 +940,7 @@ void by_vectors(const NormParams& p, const RowPlan& q, F&& f) {
   }
 }
 
-constexpr int kRowBlocks = 4, kRowBlocksBackward = 2;  // blocks an SM of the rows form
+constexpr int kRowBlocks = 3, kRowBlocksBackward = 2;  // blocks an SM of the rows form
 
 void launch_weights(const NormParams& p, const float* part, int rows, cudaStream_t st) {
   if (p.dw || p.db) norm_weights_kernel<<<(p.C + 31) / 32, dim3(32, 32), 0, st>>>(p, part, rows);
@@ -775,8 +972,8 @@ cudaError_t launch_norm_forward(const NormParams& p, cudaStream_t st) {
     constexpr int V = decltype(vec)::value;
     if (rows_form(p, v)) {
       const RowPlan q = row_plan(p, v, kRowBlocks);
-      by_vectors<V>(p, q, [&](auto nv, auto block) {
-        norm_rows_forward_kernel<T, V, decltype(nv)::value, decltype(block)::value><<<dim3(q.slices, q.blocks), kThreads, 0, st>>>(p, q);
+      by_vectors<V>(p, q, [&](auto nv, auto team) {
+        norm_rows_forward_kernel<T, V, decltype(nv)::value, decltype(team)::value><<<dim3(q.slices, q.blocks), kThreads, 0, st>>>(p, q);
       });
     } else {
       const BlockPlan q = block_plan(p, v);
@@ -786,7 +983,7 @@ cudaError_t launch_norm_forward(const NormParams& p, cudaStream_t st) {
         e = cudaErrorInvalidConfiguration;
         return;
       }
-      norm_sums_kernel<T, V><<<unsigned(grid), kThreads, kThreads * V * 8, st>>>(p, q, s.seg, s.rows_of);
+      norm_sums_kernel<T, V><<<unsigned(grid), kThreads, 0, st>>>(p, q, s.seg, s.rows_of);
       norm_apply_kernel<T, V><<<unsigned(grid), kThreads, (q.width + 1) * 8, st>>>(p, q, s.seg, s.rows_of);
     }
   });
@@ -802,8 +999,8 @@ cudaError_t launch_norm_backward(const NormParams& p, cudaStream_t st) {
     if (rows_form(p, v)) {
       const RowPlan q = row_plan(p, v, kRowBlocksBackward);
       const int shared = (q.rpi - 1) * q.gs * (p.C / p.G) * 8;
-      by_vectors<V>(p, q, [&](auto nv, auto block) {
-        auto kernel = norm_rows_backward_kernel<T, V, decltype(nv)::value, decltype(block)::value>;
+      by_vectors<V>(p, q, [&](auto nv, auto team) {
+        auto kernel = norm_rows_backward_kernel<T, V, decltype(nv)::value, decltype(team)::value>;
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, shared);
         if (e == cudaSuccess) kernel<<<dim3(q.slices, q.blocks), kThreads, shared, st>>>(p, q);
       });
