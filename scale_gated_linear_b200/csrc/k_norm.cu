@@ -312,89 +312,145 @@ __global__ void __launch_bounds__(kThreads, V * NV <= 16 ? 3 : 1) norm_rows_forw
   }
 }
 
-// Weight gradients: partial sums [blocks][2][C] (dw, db) in the workspace.
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Weight gradients: partial sums [blocks][2][C] (dw, db) in the workspace. Rows come through
+// shared memory, two ahead, each lane copying what it reads itself: held in registers, the
+// next row's 24 words beside the sums' 32 were moved behind the arithmetic or spilled (123 us
+// where this takes 80, at 65536 groups of 512).
+constexpr int kAhead = 2;
+template <typename T, int V, int NV>
+constexpr int kRowStage = kThreads * NV * 3 * (V == 1 ? 4 : 16);  // bytes of a block's rows
+
 template <typename T, int V, int NV, int TEAM>
 __global__ void __launch_bounds__(kThreads, V * NV <= 16 ? 2 : 1) norm_rows_backward_kernel(const NormParams p, const RowPlan q) {
   __shared__ float part[2][2][kThreads / 32];
-  extern __shared__ float shared[];  // [rpi - 1][gs * cg][2]
+  extern __shared__ __align__(16) uint8_t dynamic[];  // rows; in the end [rpi - 1][gs * cg][2] sums
+  constexpr bool kKeep = V * NV <= 16;  // weights in registers
   int turn = 0;
   const RowLane<T, V, NV> l(p, q);
   const int cg = p.C / p.G;
   const float inv = 1.f / cg;
   const bool gated = p.gate.ptr;
-  float dw[NV][V] = {}, db[NV][V] = {};
-  const long long step = static_cast<long long>(gridDim.y) * q.rpi;
-  long long base = static_cast<long long>(blockIdx.y) * q.rpi, row = base + l.row;
-  RowPtr<T, V> px(p.x, row, step, l.c), pd(p.dy, row, step, l.c), pg(p.gate, row, step, l.c), ox(p.dx, row, step, l.c),
-      og(p.dgate, row, step, l.c);
-  Vec<T, V> xn[NV], dn[NV], gn[NV];
-  float2 sn;
-  bool valid_next;
-  auto fetch = [&](long long r) {
-    valid_next = r < p.N && l.vectors && (!p.mask || p.mask[r]);
-    sn = valid_next ? *reinterpret_cast<const float2*>(p.stats + 2 * (r * p.G + l.g)) : make_float2(0.f, 0.f);
+  float dw[NV][V] = {}, db[NV][V] = {}, w[kKeep ? NV : 1][V], b[kKeep ? NV : 1][V];
+  if constexpr (kKeep) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const bool in = valid_next && l.in(i);
-      xn[i] = in ? load<T, V>(px.at + i * l.step) : zeros<T, V>();
-      dn[i] = in ? load<T, V>(pd.at + i * l.step) : zeros<T, V>();
-      gn[i] = in && gated ? load<T, V>(pg.at + i * l.step) : zeros<T, V>();
+      weights<V>(p.w, l.c + i * l.step, l.in(i), 1.f, w[i]);
+      weights<V>(p.b, l.c + i * l.step, l.in(i), 0.f, b[i]);
     }
+  }
+  const long long step = static_cast<long long>(gridDim.y) * q.rpi;
+  long long base = static_cast<long long>(blockIdx.y) * q.rpi, row = base + l.row, coming = row;
+  RowPtr<T, V> px(p.x, row, step, l.c), pd(p.dy, row, step, l.c), pg(p.gate, row, step, l.c), ox(p.dx, row, step, l.c),
+      og(p.dgate, row, step, l.c);
+  const float2* stats = reinterpret_cast<const float2*>(p.stats) + row * p.G + l.g;
+  const long long stat_step = step * p.G;
+  // vector i of tensor k of stage s: kThreads neighbouring words or quadruples
+  using Word = std::conditional_t<V == 1, uint32_t, uint4>;
+  Word* mine = reinterpret_cast<Word*>(dynamic) + threadIdx.x;
+  auto slot = [&](int s, int k, int i) { return mine + ((s * 3 + k) * NV + i) * kThreads; };
+  float2 st_next[kAhead];
+  uint32_t valid_bits = 0;
+  auto fetch = [&](int s) {
+    const bool valid = coming < p.N && l.vectors && (!p.mask || p.mask[coming]);
+    valid_bits = valid ? valid_bits | 1u << s : valid_bits & ~(1u << s);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const T* from = k == 0 ? px.at : k == 1 ? pd.at : pg.at;
+      if (k == 2 && !gated) break;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        Word* to = slot(s, k, i);
+        if constexpr (V == 1) {
+          *to = valid && l.in(i) ? load<T, V>(from + i * l.step).w[0] : 0u;
+        } else {
+          if (valid && l.in(i)) copy16(smem_u32(to), from + i * l.step);
+          else *to = make_uint4(0, 0, 0, 0);
+        }
+      }
+    }
+    copies_commit();
+    const float2 got = valid ? *stats : make_float2(0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      if (j == s) st_next[j] = got;
     px.at += px.step;
     pd.at += pd.step;
     pg.at += pg.step;
+    stats += stat_step;
+    coming += step;
   };
-  fetch(row);
-  for (; base < p.N; base += step, row += step, ox.at += ox.step, og.at += og.step) {
-    Vec<T, V> x[NV], d[NV], gt[NV];
-    const float2 st = sn;
-    const bool valid = valid_next, here = row < p.N;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      x[i] = xn[i];
-      d[i] = dn[i];
-      gt[i] = gn[i];
+  auto read = [&](int s, int k, int i, float (&f)[V]) {
+    Vec<T, V> v;
+    if constexpr (V == 1) {
+      v.w[0] = *slot(s, k, i);
+    } else {
+      const uint4 u = *slot(s, k, i);
+      v.w[0] = u.x, v.w[1] = u.y, v.w[2] = u.z, v.w[3] = u.w;
     }
-    if (base + step < p.N) fetch(row + step);
-    float s[2] = {0.f, 0.f}, dv[NV][V];
+    unpack(v, f);
+  };
+#pragma unroll
+  for (int s = 0; s < kAhead; ++s) fetch(s);
+  int s = 0;
+  for (; base < p.N; base += step, row += step, ox.at += ox.step, og.at += og.step) {
+    copies_wait<kAhead - 1>();
+    float2 st = st_next[0];
+#pragma unroll
+    for (int j = 1; j < kAhead; ++j)
+      if (j == s) st = st_next[j];
+    const bool valid = valid_bits >> s & 1, here = row < p.N;
+    float sums[2] = {0.f, 0.f}, dv[NV][V], xh[NV][V];
     by_act(p.act, gated, [&](auto kind, auto with_gate) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        float w[V], b[V], xv[V], dy[V], gv[V], dg[V];
-        weights<V>(p.w, l.c + i * l.step, l.in(i), 1.f, w);
-        weights<V>(p.b, l.c + i * l.step, l.in(i), 0.f, b);
-        unpack(x[i], xv);
-        unpack(d[i], dy);
-        if (with_gate) unpack(gt[i], gv);
+        float dy[V], gv[V], dg[V], wl[V], bl[V];
+        if constexpr (!kKeep) {
+          weights<V>(p.w, l.c + i * l.step, l.in(i), 1.f, wl);
+          weights<V>(p.b, l.c + i * l.step, l.in(i), 0.f, bl);
+        }
+        read(s, 0, i, xh[i]);
+        read(s, 1, i, dy);
+        if (with_gate) read(s, 2, i, gv);
 #pragma unroll
         for (int e = 0; e < V; ++e) {  // where nothing was loaded dy = 0, and with it every sum's part
-          const float xh = (xv[e] - st.x) * st.y;
-          const float t = grad_v<kind, with_gate>(fmaf(xh, w[e], b[e]), dy[e], with_gate ? gv[e] : 0.f, dg[e]);
-          dw[i][e] = fmaf(t, xh, dw[i][e]);
+          const float we = kKeep ? w[kKeep ? i : 0][e] : wl[e], be = kKeep ? b[kKeep ? i : 0][e] : bl[e];
+          xh[i][e] = (xh[i][e] - st.x) * st.y;
+          const float t = grad_v<kind, with_gate>(fmaf(xh[i][e], we, be), dy[e], with_gate ? gv[e] : 0.f, dg[e]);
+          dw[i][e] = fmaf(t, xh[i][e], dw[i][e]);
           db[i][e] += t;
-          dv[i][e] = t * w[e];
-          s[0] += dv[i][e];
-          s[1] = fmaf(dv[i][e], xh, s[1]);
+          dv[i][e] = t * we;
+          sums[0] += dv[i][e];
+          sums[1] = fmaf(dv[i][e], xh[i][e], sums[1]);
         }
         if (with_gate && here && l.in(i)) store<T, V>(og.at + i * l.step, pack<T, V>(dg));
       }
     });
-    sums_of<TEAM>(s, q.team, part, turn ^= 1);
-    const float m1 = p.center ? s[0] * inv : 0.f, m2 = s[1] * inv;
+    fetch(s);
+    s = s + 1 == kAhead ? 0 : s + 1;
+    sums_of<TEAM>(sums, q.team, part, turn ^= 1);
+    const float m1 = p.center ? sums[0] * inv : 0.f, m2 = sums[1] * inv;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      float xv[V], dx[V];
-      unpack(x[i], xv);
+      float dx[V];
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float xh = (xv[e] - st.x) * st.y;
-        dx[e] = (dv[i][e] - m1 - xh * m2) * st.y;
-      }
+      for (int e = 0; e < V; ++e) dx[e] = (dv[i][e] - m1 - xh[i][e] * m2) * st.y;
       if (here && l.in(i)) store<T, V>(ox.at + i * l.step, valid ? pack<T, V>(dx) : zeros<T, V>());
     }
   }
   if (!p.dw && !p.db) return;
   // the block's rows of every channel, summed in order by the first one's team
+  copies_wait<0>();
+  __syncthreads();
+  float* shared = reinterpret_cast<float*>(dynamic);
   const int width = q.gs * cg, c0 = blockIdx.x * width;
   if (l.row > 0) {
 #pragma unroll
@@ -564,44 +620,37 @@ __global__ void __launch_bounds__(kThreads) norm_sums_kernel(const NormParams p,
   }
 }
 
-// Joins the segments of group g of sample n (one warp): mean and 1 / sqrt(var + eps), in every lane.
+// Count, mean and sum of squared differences of two sets joined.
+struct Moments {
+  float n, mean, squares;
+  __device__ __forceinline__ void join(float m, float mu, float sq) {
+    if (m <= 0.f) return;
+    const float all = n + m, d = mu - mean, share = m / all;
+    mean = n > 0.f ? fmaf(d, share, mean) : mu;
+    squares += sq + (n > 0.f ? d * d * n * share : 0.f);
+    n = all;
+  }
+};
+// Joins the segments of group g of sample n (one warp): mean and 1 / sqrt(var + eps), in lane 0.
 __device__ __forceinline__ float2 join_stats(const NormParams& p, const BlockPlan& q, long long n, int g, const float2* seg,
                                              const float* rows_of) {
   const int cg = p.C / p.G, a = g * cg, t0 = a / q.width, segs = (a + cg - 1) / q.width - t0 + 1;
-  auto get = [&](int i, float& count) {
+  Moments m{0.f, 0.f, 0.f};
+  for (int i = lane_id(); i < segs * q.chunks; i += 32) {
     const int chunk = i / segs, t = t0 + i % segs, lo = max(a, t * q.width), hi = min(a + cg, (t + 1) * q.width);
-    count = rows_of[n * q.chunks + chunk] * (hi - lo);
-    return seg[(n * q.chunks + chunk) * p.C + lo];
-  };
-  const int all = segs * q.chunks;
-  float count = 0.f, total = 0.f, squares = 0.f, k;
-  float base = 0.f;
-  if (p.center) {  // some segment with rows, as the point to sum differences from
-    for (int i = 0; i < all; ++i) {
-      const float2 v = get(i, k);
-      if (k > 0.f) {
-        base = v.x;
-        break;
-      }
-    }
+    const float2 v = seg[(n * q.chunks + chunk) * p.C + lo];
+    m.join(rows_of[n * q.chunks + chunk] * (hi - lo), v.x, v.y);
   }
-  for (int i = lane_id(); i < all; i += 32) {
-    const float2 v = get(i, k);
-    count += k;
-    if (k > 0.f) total = fmaf(k, v.x - base, total);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    const float k = __shfl_down_sync(~0u, m.n, o), mu = __shfl_down_sync(~0u, m.mean, o), sq = __shfl_down_sync(~0u, m.squares, o);
+    m.join(k, mu, sq);
   }
-  count = fmaxf(team_sum(count, 32), 1.f);
-  const float mean = p.center ? base + team_sum(total, 32) / count : 0.f;
-  for (int i = lane_id(); i < all; i += 32) {
-    const float2 v = get(i, k);
-    const float d = v.x - mean;
-    if (k > 0.f) squares += v.y + k * d * d;
-  }
-  return make_float2(mean, 1.f / sqrtf(team_sum(squares, 32) / count + p.eps));
+  return make_float2(p.center ? m.mean : 0.f, 1.f / sqrtf(m.squares / fmaxf(m.n, 1.f) + p.eps));
 }
 
 template <typename T, int V>
-__global__ void __launch_bounds__(kThreads) norm_apply_kernel(const NormParams p, const BlockPlan q, const float2* seg,
+__global__ void __launch_bounds__(kThreads, 3) norm_apply_kernel(const NormParams p, const BlockPlan q, const float2* seg,
                                                               const float* rows_of) {
   extern __shared__ float2 stat[];  // groups that meet the tile
   const Part part(q);
@@ -616,14 +665,12 @@ __global__ void __launch_bounds__(kThreads) norm_apply_kernel(const NormParams p
   }
   __syncthreads();
   if (c >= p.C) return;
-  float mean[V], w[V], b[V];
+  const float2 st = stat[c / cg - g0];  // a vector's channels are of one group
+  float w[V], b[V];
+  weights<V>(p.w, c, true, 1.f, w);
+  weights<V>(p.b, c, true, 0.f, b);
 #pragma unroll
-  for (int e = 0; e < V; ++e) {
-    const float2 v = stat[(c + e) / cg - g0];
-    mean[e] = v.x;
-    w[e] = v.y * (p.w ? p.w[c + e] : 1.f);
-    b[e] = p.b ? p.b[c + e] : 0.f;
-  }
+  for (int e = 0; e < V; ++e) w[e] *= st.y;
   const long long s0 = static_cast<long long>(part.chunk) * q.rows, s1 = min(s0 + q.rows, p.S);
   const uint8_t* m = p.mask ? p.mask + part.n * p.S : nullptr;
   const T* xp = at<T>(p.x, part.n, 0, c);
@@ -648,7 +695,7 @@ __global__ void __launch_bounds__(kThreads) norm_apply_kernel(const NormParams p
           if (gated) unpack(gt[k], gv);
 #pragma unroll
           for (int e = 0; e < V; ++e) {
-            const float v = fmaf(xv[e] - mean[e], w[e], b[e]);
+            const float v = fmaf(xv[e] - st.x, w[e], b[e]);
             r[e] = gated ? v * act<kind>(gv[e]) : act<kind>(v);
           }
           y = pack<T, V>(r);
@@ -662,7 +709,7 @@ __global__ void __launch_bounds__(kThreads) norm_apply_kernel(const NormParams p
 // Backward sums: per channel dw and db of every (n, chunk) as chan[(n * chunks + chunk)][2][C], per
 // segment (sum dv w, sum dv w xhat) as seg, and the valid rows.
 template <typename T, int V>
-__global__ void __launch_bounds__(kThreads) norm_grad_sums_kernel(const NormParams p, const BlockPlan q, float* chan, float2* seg,
+__global__ void __launch_bounds__(kThreads, 2) norm_grad_sums_kernel(const NormParams p, const BlockPlan q, float* chan, float2* seg,
                                                                   float* rows_of) {
   extern __shared__ float2 cell[];  // [ty][width]
   __shared__ int counts[kThreads];
@@ -671,17 +718,12 @@ __global__ void __launch_bounds__(kThreads) norm_grad_sums_kernel(const NormPara
   const long long s0 = static_cast<long long>(part.chunk) * q.rows, s1 = min(s0 + q.rows, p.S);
   const uint8_t* m = p.mask ? p.mask + part.n * p.S : nullptr;
   const size_t at_part = static_cast<size_t>(part.n) * q.chunks + part.chunk;
-  float mean[V], rstd[V], w[V], b[V], dw[V] = {}, db[V] = {};
+  float w[V], b[V], dw[V] = {}, db[V] = {};
   int count = 0;
   if (c < p.C) {
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const float2 v = *reinterpret_cast<const float2*>(p.stats + 2 * (part.n * p.G + (c + e) / cg));
-      mean[e] = v.x;
-      rstd[e] = v.y;
-      w[e] = p.w ? p.w[c + e] : 1.f;
-      b[e] = p.b ? p.b[c + e] : 0.f;
-    }
+    const float2 st = *reinterpret_cast<const float2*>(p.stats + 2 * (part.n * p.G + c / cg));
+    weights<V>(p.w, c, true, 1.f, w);
+    weights<V>(p.b, c, true, 0.f, b);
     const T* xp = at<T>(p.x, part.n, 0, c);
     const T* dp = at<T>(p.dy, part.n, 0, c);
     const T* gp = at<T>(p.gate, part.n, 0, c);
@@ -706,7 +748,7 @@ __global__ void __launch_bounds__(kThreads) norm_grad_sums_kernel(const NormPara
             if (gated) unpack(gt[k], gv);
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-              const float xh = (xv[e] - mean[e]) * rstd[e];
+              const float xh = (xv[e] - st.x) * st.y;
               const float t = grad_v<kind, gated>(fmaf(xh, w[e], b[e]), dy[e], gated ? gv[e] : 0.f, dg);
               dw[e] = fmaf(t, xh, dw[e]);
               db[e] += t;
@@ -753,7 +795,7 @@ __global__ void __launch_bounds__(kThreads) norm_grad_sums_kernel(const NormPara
 }
 
 template <typename T, int V>
-__global__ void __launch_bounds__(kThreads) norm_grad_apply_kernel(const NormParams p, const BlockPlan q, const float2* seg,
+__global__ void __launch_bounds__(kThreads, 2) norm_grad_apply_kernel(const NormParams p, const BlockPlan q, const float2* seg,
                                                                    const float* rows_of) {
   extern __shared__ float2 stat[];  // <dv w>, <dv w xhat> of the groups that meet the tile
   const Part part(q);
@@ -776,18 +818,10 @@ __global__ void __launch_bounds__(kThreads) norm_grad_apply_kernel(const NormPar
   }
   __syncthreads();
   if (c >= p.C) return;
-  float mean[V], rstd[V], w[V], b[V], m1[V], m2[V];
-#pragma unroll
-  for (int e = 0; e < V; ++e) {
-    const int g = (c + e) / cg;
-    const float2 v = *reinterpret_cast<const float2*>(p.stats + 2 * (part.n * p.G + g));
-    mean[e] = v.x;
-    rstd[e] = v.y;
-    w[e] = p.w ? p.w[c + e] : 1.f;
-    b[e] = p.b ? p.b[c + e] : 0.f;
-    m1[e] = stat[g - g0].x;
-    m2[e] = stat[g - g0].y;
-  }
+  const float2 st = *reinterpret_cast<const float2*>(p.stats + 2 * (part.n * p.G + c / cg)), mm = stat[c / cg - g0];
+  float w[V], b[V];
+  weights<V>(p.w, c, true, 1.f, w);
+  weights<V>(p.b, c, true, 0.f, b);
   const long long s0 = static_cast<long long>(part.chunk) * q.rows, s1 = min(s0 + q.rows, p.S);
   const uint8_t* m = p.mask ? p.mask + part.n * p.S : nullptr;
   const T* xp = at<T>(p.x, part.n, 0, c);
@@ -816,9 +850,9 @@ __global__ void __launch_bounds__(kThreads) norm_grad_apply_kernel(const NormPar
           if (gated) unpack(gt[k], gv);
 #pragma unroll
           for (int e = 0; e < V; ++e) {
-            const float xh = (xv[e] - mean[e]) * rstd[e];
+            const float xh = (xv[e] - st.x) * st.y;
             const float t = grad_v<kind, gated>(fmaf(xh, w[e], b[e]), dy[e], gated ? gv[e] : 0.f, dg[e]) * w[e];
-            r[e] = (t - m1[e] - xh * m2[e]) * rstd[e];
+            r[e] = (t - mm.x - xh * mm.y) * st.y;
           }
           dx = pack<T, V>(r);
           if (gated) dgate = pack<T, V>(dg);
@@ -998,9 +1032,10 @@ cudaError_t launch_norm_backward(const NormParams& p, cudaStream_t st) {
     constexpr int V = decltype(vec)::value;
     if (rows_form(p, v)) {
       const RowPlan q = row_plan(p, v, kRowBlocksBackward);
-      const int shared = (q.rpi - 1) * q.gs * (p.C / p.G) * 8;
+      const int sums = (q.rpi - 1) * q.gs * (p.C / p.G) * 8;
       by_vectors<V>(p, q, [&](auto nv, auto team) {
         auto kernel = norm_rows_backward_kernel<T, V, decltype(nv)::value, decltype(team)::value>;
+        const int rows = kAhead * kRowStage<T, V, decltype(nv)::value>, shared = rows > sums ? rows : sums;
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, shared);
         if (e == cudaSuccess) kernel<<<dim3(q.slices, q.blocks), kThreads, shared, st>>>(p, q);
       });
