@@ -68,6 +68,10 @@ struct Pair<__nv_bfloat16> {
     const float2 f = f2_unpack(v);
     return pack_bf162(f.x, f.y);
   }
+  static __device__ __forceinline__ Raw least(Raw a, Raw b) {
+    const __nv_bfloat162 m = __hmin2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+    return *reinterpret_cast<const Raw*>(&m);
+  }
   static __device__ __forceinline__ Raw join(__nv_bfloat16 a, __nv_bfloat16 b) {
     return uint32_t(__bfloat16_as_ushort(a)) | uint32_t(__bfloat16_as_ushort(b)) << 16;
   }
@@ -87,6 +91,10 @@ struct Pair<__half> {
   static __device__ __forceinline__ Raw round(uint64_t v) {
     const float2 f = f2_unpack(v);
     return pack_half2(f.x, f.y);
+  }
+  static __device__ __forceinline__ Raw least(Raw a, Raw b) {
+    const __half2 m = __hmin2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+    return *reinterpret_cast<const Raw*>(&m);
   }
   static __device__ __forceinline__ Raw join(__half a, __half b) {
     return uint32_t(__half_as_ushort(a)) | uint32_t(__half_as_ushort(b)) << 16;
@@ -187,24 +195,25 @@ __device__ __forceinline__ void expm1_small(const uint64_t (&s)[K], const DecayP
   for (int k = 0; k < K; ++k) r[k] = f2_mul(s[k], r[k]);
 }
 
-// Whether -c comes from the expansion, and so has a `far` to look at.
-template <typename T, bool TAU1>
-constexpr bool kExpansion = sizeof(T) == 2 && !TAU1;
-
-// -c of K pairs of logits. With S = softplus(-z), -c = e^{-S / tau} - 1 is S times a
-// polynomial in S while S <= tau / 2; `far` takes the largest S of the calls, beyond that bound
-// neg_decay_far has to be called. For f32 tensors the library functions: their callers
-// compare 24 bits, and 12 bytes an element leave time. TAU1: c = 1 - sigmoid(z) in closed form.
-template <typename T, bool TAU1, int K>
-__device__ __forceinline__ void neg_decay(const uint64_t (&z)[K], const DecayParams& g, float& far, uint64_t (&nc)[K]) {
-  if constexpr (kExpansion<T, TAU1>) {
+// -c of K pairs of logits. With S = softplus(-z), -c = e^{-S / tau} - 1 is S times a polynomial in S
+// while S <= tau / 2; beyond (FAR: look for it), where e^{-S / tau} < 0.61 loses nothing in the
+// difference from one, it is that difference. For f32 tensors the library functions: their
+// callers compare 24 bits, and 12 bytes an element leave time. TAU1: c = 1 - sigmoid(z) in closed form.
+template <typename T, bool TAU1, bool FAR, int K>
+__device__ __forceinline__ void neg_decay(const uint64_t (&z)[K], const DecayParams& g, uint64_t (&nc)[K]) {
+  if constexpr (sizeof(T) == 2 && !TAU1) {
     uint64_t s[K];
     softplus_neg(z, s);
     expm1_small(s, g, nc);
+    if constexpr (FAR) {
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const float2 f = f2_unpack(s[k]);
-      far = fmaxf(far, fmaxf(f.x, f.y));
+      for (int k = 0; k < K; ++k) {
+        const float2 f = f2_unpack(s[k]);
+        float2 n = f2_unpack(nc[k]);
+        if (f.x > g.far) n.x = ex2_approx(-kLog2e * g.inv_tau * f.x) - 1.f;
+        if (f.y > g.far) n.y = ex2_approx(-kLog2e * g.inv_tau * f.y) - 1.f;
+        nc[k] = f2_pack(n.x, n.y);
+      }
     }
   } else {
 #pragma unroll
@@ -226,37 +235,34 @@ __device__ __forceinline__ void neg_decay(const uint64_t (&z)[K], const DecayPar
     }
   }
 }
-// -c where S may be large: e^{-S / tau} < 0.61 loses nothing in the difference from one.
-__device__ __forceinline__ uint64_t neg_decay_far(uint64_t z, const DecayParams& g) {
-  uint64_t zz[1] = {z}, s[1], r[1];
-  softplus_neg(zz, s);
-  expm1_small(s, g, r);
-  const float2 sf = f2_unpack(s[0]);
-  float2 n = f2_unpack(r[0]);
-  if (sf.x > g.far) n.x = ex2_approx(-kLog2e * g.inv_tau * sf.x) - 1.f;
-  if (sf.y > g.far) n.y = ex2_approx(-kLog2e * g.inv_tau * sf.y) - 1.f;
-  return f2_pack(n.x, n.y);
-}
 
-// -c of a warp's R rows of logits in shared memory, K pairs at a time.
+// -c of a warp's R rows of logits in shared memory, K pairs at a time. Whether some S is beyond the
+// expansion is seen from the smallest logit, before anything is computed.
 template <typename T, bool TAU1, int R>
 __device__ __forceinline__ void row_decays(const typename Pair<T>::Raw* zs, const DecayParams& g, uint64_t (&nc)[R]) {
   using P = Pair<T>;
-  constexpr int K = kExpansion<T, TAU1> ? 4 : 2;
-  float far = 0.f;
+  constexpr int K = sizeof(T) == 2 ? 4 : 2;
+  auto rows = [&](auto far) {
 #pragma unroll
-  for (int r = 0; r < R; r += K) {
-    uint64_t z[K], v[K];
+    for (int r = 0; r < R; r += K) {
+      uint64_t z[K], v[K];
 #pragma unroll
-    for (int k = 0; k < K; ++k) z[k] = P::f32(zs[(r + k) * 32]);
-    neg_decay<T, TAU1>(z, g, far, v);
+      for (int k = 0; k < K; ++k) z[k] = P::f32(zs[(r + k) * 32]);
+      neg_decay<T, TAU1, decltype(far)::value>(z, g, v);
 #pragma unroll
-    for (int k = 0; k < K; ++k) nc[r + k] = v[k];
+      for (int k = 0; k < K; ++k) nc[r + k] = v[k];
+    }
+  };
+  bool far = false;
+  if constexpr (sizeof(T) == 2 && !TAU1) {
+    typename P::Raw least = zs[0];
+#pragma unroll
+    for (int r = 1; r < R; ++r) least = P::least(least, zs[r * 32]);
+    const float2 f = f2_unpack(P::f32(least));
+    far = fminf(f.x, f.y) < g.far_logit;
   }
-  if (kExpansion<T, TAU1> && far > g.far) {
-#pragma unroll
-    for (int r = 0; r < R; ++r) nc[r] = neg_decay_far(P::f32(zs[r * 32]), g);
-  }
+  if (far) rows(std::true_type{});
+  else rows(std::false_type{});
 }
 
 // a (1 - sigmoid(z)) / tau, for padded rows (z = +inf, c = 0) zero
@@ -302,14 +308,31 @@ __device__ __forceinline__ void send_join(Join* slots, int rank, int cluster, co
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// Bits of the valid rows t0 .. t0 + R - 1 (bit r: row t0 + r).
+// The valid rows of the chunks a warp takes one after another. The mask of a chunk decides which
+// copies are started, so its bytes are loaded one chunk earlier still (the copies
+// waited for them otherwise: 6 us of a forward of 8 x 2048 x 2048).
 template <int R>
-__device__ __forceinline__ uint32_t valid_rows(const uint8_t* m, int t0, int L) {
-  const int n = min(max(L - t0, 0), R);
-  if (!m) return (1u << n) - 1u;
-  const int r = lane_id();
-  return __ballot_sync(~0u, r < n && m[t0 + r] != 0);
-}
+struct ValidRows {
+  const uint8_t* mask;  // of the sequence, or null
+  int L, ahead;
+  __device__ __forceinline__ ValidRows(const ScanParams& p, int b) : mask(p.mask), L(p.L), ahead(0) {
+    if (mask) mask += static_cast<size_t>(b) * L;
+  }
+  __device__ __forceinline__ void look(int t0) {  // rows t0 .. t0 + R - 1 come next
+    const int t = t0 + lane_id();
+    if (mask) ahead = lane_id() < R && t >= 0 && t < L ? mask[t] : 0;
+  }
+  // bit r: row t0 + r, the rows looked at last; then looks at those from `next` on
+  __device__ __forceinline__ uint32_t take(int t0, int next) {
+    if (!mask) {
+      const int n = t0 < 0 ? 0 : min(max(L - t0, 0), R);
+      return (1u << n) - 1u;
+    }
+    const uint32_t bits = __ballot_sync(~0u, ahead != 0);
+    look(next);
+    return bits;
+  }
+};
 
 // ---------------------------------------------------------------- rows in shared memory
 // A warp's R rows of 64 channels take 2 KB for every type (16 rows of 128 bytes, 8 of 256).
@@ -420,7 +443,6 @@ __global__ void __launch_bounds__(kWarps * 32, 3) scan_forward_kernel(const Scan
   const int w = warp_id(), lane = lane_id(), b = blockIdx.y;
   const int c0 = blockIdx.x / cluster * 64, ch = c0 + 2 * lane, n = min(max(p.D - ch, 0), 2);
   uint8_t* mine = dynamic + w * kStages * 2 * kRowsBytes;
-  const uint8_t* m = p.mask ? p.mask + static_cast<size_t>(b) * p.L : nullptr;
   const size_t state_at = static_cast<size_t>(b) * p.D + ch;
   const int chunks = (p.L + R - 1) / R, steps = (p.L + cluster * kRows - 1) / (cluster * kRows);
 
@@ -429,10 +451,12 @@ __global__ void __launch_bounds__(kWarps * 32, 3) scan_forward_kernel(const Scan
   Lane<T, VEC> lx(p.x, b, c0, p.D), lz(p.z, b, c0, p.D), lo(p.h, b, c0, p.D);
   const int first = (rank * kWarps + w) * R;
   lx.move(first), lz.move(first), lo.move(first);
+  ValidRows<R> valid(p, b);
+  valid.look(first);
   auto start_step = [&](int step) {
     if (step < steps) {
       uint8_t* to = mine + step % kStages * 2 * kRowsBytes;
-      coming = valid_rows<R>(m, first + step * cluster * kRows, p.L);
+      coming = valid.take(first + step * cluster * kRows, first + (step + 1) * cluster * kRows);
       const bool full = inside && coming == (1u << R) - 1u;
       fetch<T, VEC>(to, lx, full, coming, P::zero());
       fetch<T, VEC>(to + kRowsBytes, lz, full, coming, P::inf());
@@ -528,16 +552,17 @@ __global__ void __launch_bounds__(kRelay * 32, 2) scan_relay_kernel(const ScanPa
   const int chunks = (p.L + R - 1) / R;
   const bool inside = c0 + 64 <= p.D;
   const size_t state_at = static_cast<size_t>(b) * p.D + ch;
-  const uint8_t* m = p.mask ? p.mask + static_cast<size_t>(b) * p.L : nullptr;
   uint8_t* mine = dynamic + w * 4 * kRowsBytes;
   float* saved = p.saved ? p.saved + (static_cast<size_t>(b) * chunks + w) * p.D + ch : nullptr;
   Lane<T, VEC> lx(p.x, b, c0, p.D), lz(p.z, b, c0, p.D), lo(p.h, b, c0, p.D);
   lx.move(w * R), lz.move(w * R), lo.move(w * R);
+  ValidRows<R> valid(p, b);
+  valid.look(w * R);
   auto start = [&](int c, int slot) {
     uint32_t bits = 0;
     if (c < chunks) {
       uint8_t* to = mine + slot * 2 * kRowsBytes;
-      bits = !m && (c + 1) * R <= p.L ? kFull : valid_rows<R>(m, c * R, p.L);
+      bits = valid.take(c * R, (c + kRelay) * R);
       const bool full = inside && bits == kFull;
       fetch<T, VEC>(to, lx, full, bits, P::zero());
       fetch<T, VEC>(to + kRowsBytes, lz, full, bits, P::inf());
@@ -597,20 +622,32 @@ __global__ void __launch_bounds__(kRelay * 32, 2) scan_relay_kernel(const ScanPa
 // Chunks of R rows, from the last. A chunk's states are rebuilt from its saved one, so
 // everything but g is independent of the other chunks: per row -c and
 // q = (h_{t-1} - [tied] x_t) a_t (1 - sigmoid(z_t)) / tau. Then, down the rows,
-// g_t = dh_t + in, dz_t = g_t q_t, in = a_t g_t.
+// g_t = dh_t + in, dz_t = g_t q_t, in = a_t g_t. q takes the place of x and z in shared
+// memory (with -c and q of 16 rows in registers, 64 of them, the kernels spilled).
 template <typename T, bool TAU1, bool TIED>
-__device__ __forceinline__ void row_factors(const typename Pair<T>::Raw* xs, const typename Pair<T>::Raw* zs, uint64_t h,
-                                            const DecayParams& gate, uint64_t (&nc)[kRowsOf<T>],
-                                            uint64_t (&q)[kRowsOf<T>]) {
+__device__ __forceinline__ void row_factors(typename Pair<T>::Raw* xs, typename Pair<T>::Raw* zs, uint64_t h,
+                                            const DecayParams& gate, uint64_t (&nc)[kRowsOf<T>]) {
   using P = Pair<T>;
   constexpr int R = kRowsOf<T>;
   row_decays<T, TAU1>(zs, gate, nc);
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const uint64_t x = P::f32(xs[r * 32]);
-    q[r] = f2_mul(TIED ? f2_add(h, f2_neg(x)) : h, decay_slope<T>(P::f32(zs[r * 32]), nc[r], gate.inv_tau));
+    const uint64_t q = f2_mul(TIED ? f2_add(h, f2_neg(x)) : h, decay_slope<T>(P::f32(zs[r * 32]), nc[r], gate.inv_tau));
     h = advance<TIED>(h, nc[r], x);
+    if constexpr (sizeof(T) == 4) {
+      xs[r * 32] = q;
+    } else {
+      const float2 f = f2_unpack(q);
+      xs[r * 32] = __float_as_uint(f.x);
+      zs[r * 32] = __float_as_uint(f.y);
+    }
   }
+}
+template <typename T>
+__device__ __forceinline__ uint64_t get_factor(const typename Pair<T>::Raw* xs, const typename Pair<T>::Raw* zs) {
+  if constexpr (sizeof(T) == 4) return *xs;
+  else return f2_pack(__uint_as_float(*xs), __uint_as_float(*zs));
 }
 template <bool TIED>
 __device__ __forceinline__ uint64_t input_grad(uint64_t nc, uint64_t g) {
@@ -619,7 +656,7 @@ __device__ __forceinline__ uint64_t input_grad(uint64_t nc, uint64_t g) {
 
 // One block per tile, as the forward, with the chunks from the last and the relay going that
 // way: a chunk hands down out = P in + G.
-constexpr int kBackRelay = 9;
+constexpr int kBackRelay = 8;
 constexpr int kBackRelayShared = kBackRelay * 2 * 3 * kRowsBytes;
 
 template <typename T, bool VEC, bool TAU1, bool TIED>
@@ -635,17 +672,18 @@ __global__ void __launch_bounds__(kBackRelay * 32, 2) scan_relay_backward_kernel
   const int chunks = (p.L + R - 1) / R;
   const bool inside = c0 + 64 <= p.D;
   const size_t state_at = static_cast<size_t>(b) * p.D + ch;
-  const uint8_t* m = p.mask ? p.mask + static_cast<size_t>(b) * p.L : nullptr;
   uint8_t* mine = dynamic + w * 6 * kRowsBytes;
   Lane<T, VEC> lx(p.x, b, c0, p.D), lz(p.z, b, c0, p.D), ld(p.dh, b, c0, p.D), ox(p.dx, b, c0, p.D), oz(p.dz, b, c0, p.D);
   const int first = (chunks - 1 - w) * R;  // below zero where the warp has no chunk: then it is not used
   lx.move(first), lz.move(first), ld.move(first), ox.move(first), oz.move(first);
+  ValidRows<R> valid(p, b);
+  valid.look(first);
   uint64_t state = 0ull;
   auto start = [&](int c, int slot) {
     uint32_t bits = 0;
     if (c >= 0) {
       uint8_t* to = mine + slot * 3 * kRowsBytes;
-      bits = !m && (c + 1) * R <= p.L ? kFull : valid_rows<R>(m, c * R, p.L);
+      bits = valid.take(c * R, (c - kBackRelay) * R);
       const bool full = inside && bits == kFull;
       fetch<T, VEC>(to, lx, full, bits, P::zero());
       fetch<T, VEC>(to + kRowsBytes, lz, full, bits, P::inf());
@@ -666,8 +704,8 @@ __global__ void __launch_bounds__(kBackRelay * 32, 2) scan_relay_backward_kernel
     Raw* xs = reinterpret_cast<Raw*>(rows) + lane;
     Raw* zs = xs + kRowsBytes / sizeof(Raw);
     const Raw* ds = zs + kRowsBytes / sizeof(Raw);
-    uint64_t nc[R], q[R];
-    row_factors<T, TAU1, TIED>(xs, zs, before, p.gate, nc, q);
+    uint64_t nc[R];
+    row_factors<T, TAU1, TIED>(xs, zs, before, p.gate, nc);
     Join join{f2_both(1.f), 0ull};
 #pragma unroll
     for (int r = R - 1; r >= 0; --r) {
@@ -692,10 +730,10 @@ __global__ void __launch_bounds__(kBackRelay * 32, 2) scan_relay_backward_kernel
     }
 #pragma unroll
     for (int r = R - 1; r >= 0; --r) {
-      const uint64_t g = f2_add(in, P::f32(ds[r * 32]));
+      const uint64_t g = f2_add(in, P::f32(ds[r * 32])), q = get_factor<T>(xs + r * 32, zs + r * 32);
       in = f2_fma(nc[r], g, g);
       xs[r * 32] = P::round(input_grad<TIED>(nc[r], g));
-      zs[r * 32] = P::round(f2_mul(g, q[r]));
+      zs[r * 32] = P::round(f2_mul(g, q));
     }
     __syncwarp();
     const bool full = inside && now == kFull;
@@ -723,7 +761,6 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_backward_kernel(const Sca
   const int w = warp_id(), lane = lane_id(), b = blockIdx.y;
   const int c0 = blockIdx.x / cluster * 64, ch = c0 + 2 * lane, n = min(max(p.D - ch, 0), 2);
   uint8_t* mine = dynamic + w * 2 * 3 * kRowsBytes;
-  const uint8_t* m = p.mask ? p.mask + static_cast<size_t>(b) * p.L : nullptr;
   const size_t state_at = static_cast<size_t>(b) * p.D + ch;
   const int chunks = (p.L + R - 1) / R, steps = (chunks + cluster * kWarps - 1) / (cluster * kWarps);
   const float* saved = p.saved + static_cast<size_t>(b) * chunks * p.D + ch;
@@ -734,11 +771,13 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_backward_kernel(const Sca
   Lane<T, VEC> lx(p.x, b, c0, p.D), lz(p.z, b, c0, p.D), ld(p.dh, b, c0, p.D), ox(p.dx, b, c0, p.D), oz(p.dz, b, c0, p.D);
   const int first = (chunks - 1 - (rank * kWarps + w)) * R, back = -cluster * kWarps * R;
   lx.move(first), lz.move(first), ld.move(first), ox.move(first), oz.move(first);
+  ValidRows<R> valid(p, b);
+  valid.look(first);
   auto start_step = [&](int step) {
     const int c = chunks - 1 - ((step * cluster + rank) * kWarps + w);
     coming = 0;
     if (step < steps) {  // with c < 0 no row is valid and nothing is read
-      if (c >= 0) coming = valid_rows<R>(m, c * R, p.L);
+      coming = valid.take(c * R, c * R + back);
       uint8_t* to = mine + (step & 1) * 3 * kRowsBytes;
       const bool full = inside && coming == (1u << R) - 1u;
       fetch<T, VEC>(to, lx, full, coming, P::zero());
@@ -765,8 +804,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_backward_kernel(const Sca
     Raw* xs = reinterpret_cast<Raw*>(rows) + lane;
     Raw* zs = xs + kRowsBytes / sizeof(Raw);
     const Raw* ds = zs + kRowsBytes / sizeof(Raw);
-    uint64_t nc[R], q[R];
-    row_factors<T, TAU1, TIED>(xs, zs, h, p.gate, nc, q);
+    uint64_t nc[R];
+    row_factors<T, TAU1, TIED>(xs, zs, h, p.gate, nc);
     Join join{f2_both(1.f), 0ull};
 #pragma unroll
     for (int r = R - 1; r >= 0; --r) {
@@ -805,10 +844,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_backward_kernel(const Sca
     }
 #pragma unroll
     for (int r = R - 1; r >= 0; --r) {
-      const uint64_t g = f2_add(in, P::f32(ds[r * 32]));
+      const uint64_t g = f2_add(in, P::f32(ds[r * 32])), q = get_factor<T>(xs + r * 32, zs + r * 32);
       in = f2_fma(nc[r], g, g);
       xs[r * 32] = P::round(input_grad<TIED>(nc[r], g));
-      zs[r * 32] = P::round(f2_mul(g, q[r]));
+      zs[r * 32] = P::round(f2_mul(g, q));
     }
     __syncwarp();
     if (c >= 0) {
@@ -832,11 +871,9 @@ __global__ void __launch_bounds__(128) scan_step_kernel(const StepParams p) {
     float* s = p.state + static_cast<size_t>(b) * p.D + ch;
     const uint64_t z = P::f32(load_pair<T, VEC>(static_cast<const T*>(p.z) + b * p.z_row + ch, n, P::inf()));
     const uint64_t x = P::f32(load_pair<T, VEC>(static_cast<const T*>(p.x) + b * p.x_row + ch, n, P::zero()));
-    float far = 0.f;
     const uint64_t zz[1] = {z};
     uint64_t nc[1];
-    neg_decay<T, TAU1>(zz, p.gate, far, nc);
-    if (kExpansion<T, TAU1> && far > p.gate.far) nc[0] = neg_decay_far(z, p.gate);
+    neg_decay<T, TAU1, true>(zz, p.gate, nc);
     const uint64_t h = advance<TIED>(load_state<VEC>(s, n), nc[0], x);
     store_state<VEC>(s, n, h);
     out = P::round(h);
@@ -893,6 +930,7 @@ DecayParams decay_params(float inv_tau) {
   DecayParams g;
   g.inv_tau = inv_tau;
   g.far = 0.5f / inv_tau;
+  g.far_logit = static_cast<float>(-std::log(std::expm1(0.5 / inv_tau)));  // softplus(-z) = far; -inf for large tau
   double power = inv_tau;
   for (int i = 0; i < 5; ++i, power *= inv_tau) g.expm1[i] = make_float2(static_cast<float>(k[i] * power), static_cast<float>(k[i] * power));
   return g;

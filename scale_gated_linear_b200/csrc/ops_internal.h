@@ -22,10 +22,11 @@ struct Rows {
 // ---------------------------------------------------------------- gated recurrence
 int scan_saved_rows(int dtype);  // rows between two saved states
 
-// The gate as its kernels use it (set by the launches): 1 / tau, tau / 2, and the
-// polynomial of (e^{-S / tau} - 1) / S, both halves of every packed operand.
+// The gate as its kernels use it (set by the launches): 1 / tau; far = tau / 2 and the logit
+// where softplus(-z) is that; the polynomial of (e^{-S / tau} - 1) / S, both halves of every
+// packed operand.
 struct DecayParams {
-  float inv_tau, far;
+  float inv_tau, far, far_logit;
   float2 expm1[5];
 };
 
