@@ -26,8 +26,7 @@
 // and passes the joined pairs through distributed shared memory, one cluster barrier a
 // step. The next step's rows are loaded before this step's are joined.
 #include <cmath>
-#include <cstdlib>
-#include <cstring>
+#include <mutex>
 #include <type_traits>
 
 #include "ops_internal.h"
@@ -36,7 +35,8 @@
 namespace msgla {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLog2eLow = 1.4426950408889634 - static_cast<double>(kLog2e);
+constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kMaxCluster = 8;
 
 __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
@@ -110,6 +110,10 @@ struct Pair<float> {
   static __device__ __forceinline__ Raw inf() { return 0x7f8000007f800000ull; }
   static __device__ __forceinline__ uint64_t f32(Raw r) { return r; }
   static __device__ __forceinline__ Raw round(uint64_t v) { return v; }
+  static __device__ __forceinline__ Raw least(Raw a, Raw b) {
+    const float2 f = f2_unpack(a), g = f2_unpack(b);
+    return f2_pack(fminf(f.x, g.x), fminf(f.y, g.y));
+  }
   static __device__ __forceinline__ Raw join(float a, float b) { return f2_pack(a, b); }
   static __device__ __forceinline__ float half(Raw r, int i) {
     const float2 f = f2_unpack(r);
@@ -153,29 +157,53 @@ __device__ __forceinline__ void store_state(float* p, int n, uint64_t v) {
 }
 
 // ---------------------------------------------------------------- the gate
-// log(1 + e) / e on [0, 1]: a Chebyshev expansion cut off at degree 7 (relative error 2.4e-7,
-// computed in 64 bits). Both halves of the packed operands stand in constant memory.
-__constant__ float2 kLog1p[8] = {
+// log(1 + e) / e on [0, 1]: Chebyshev expansions computed in 64 bits, cut off at degree 7 for 16-bit
+// tensors (relative error 2.4e-7) and at 9 for f32 (6e-9, and roundings). Both halves of
+// the packed operands stand in constant memory.
+__constant__ float2 kLog1p7[8] = {
     {0.999999762f, 0.999999762f},   {-0.499971271f, -0.499971271f}, {0.332711875f, 0.332711875f},
     {-0.244704694f, -0.244704694f}, {0.176754937f, 0.176754937f},   {-0.106677905f, -0.106677905f},
     {0.0433708504f, 0.0433708504f}, {-0.00833649747f, -0.00833649747f}};
+__constant__ float2 kLog1p9[10] = {
+    {1.f, 1.f},                       {-0.499998897f, -0.499998897f}, {0.333296657f, 0.333296657f},
+    {-0.249511674f, -0.249511674f},   {0.196610183f, 0.196610183f},   {-0.152632743f, -0.152632743f},
+    {0.105329506f, 0.105329506f},     {-0.0562695265f, -0.0562695265f}, {0.0194876865f, 0.0194876865f},
+    {-0.00316399941f, -0.00316399941f}};
+template <typename T>
+constexpr int kDegree = sizeof(T) == 4 ? 9 : 7;
+template <typename T>
+constexpr int kExpDegree = sizeof(T) == 4 ? 5 : 4;
 __device__ __forceinline__ uint64_t f2_const(const float2& v) { return *reinterpret_cast<const uint64_t*>(&v); }
+template <typename T>
+__device__ __forceinline__ uint64_t log1p_term(int i) {
+  if constexpr (sizeof(T) == 4) return f2_const(kLog1p9[i]);
+  else return f2_const(kLog1p7[i]);
+}
+// e^{-|z|}. For f32 tensors with what the product -|z| log2(e) rounds off (at z = 60 that is 2^-18 of
+// the result; a 16-bit logit's own step is far coarser).
+template <typename T>
+__device__ __forceinline__ float exp_neg_abs(float z) {
+  const float hi = -kLog2e * fabsf(z);
+  if constexpr (sizeof(T) == 2) return ex2_approx(hi);
+  const float lo = fmaf(-kLog2eLow, fabsf(z), fmaf(-kLog2e, fabsf(z), -hi)), e = ex2_approx(hi);
+  return hi > -126.f ? fmaf(e, lo * kLn2, e) : e;  // also keeps inf - inf out
+}
 // softplus(-z) of K pairs. The K are taken through every operation together: one pair's
-// operations wait for each other, and a scheduler has four warps to fill the gaps.
-template <int K>
+// operations wait for each other, and a scheduler has few warps to fill the gaps.
+template <typename T, int K>
 __device__ __forceinline__ void softplus_neg(const uint64_t (&z)[K], uint64_t (&s)[K]) {
   uint64_t e[K];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const float2 f = f2_unpack(z[k]);
-    e[k] = f2_pack(ex2_approx(-kLog2e * fabsf(f.x)), ex2_approx(-kLog2e * fabsf(f.y)));
+    e[k] = f2_pack(exp_neg_abs<T>(f.x), exp_neg_abs<T>(f.y));
   }
 #pragma unroll
-  for (int k = 0; k < K; ++k) s[k] = f2_const(kLog1p[7]);
+  for (int k = 0; k < K; ++k) s[k] = log1p_term<T>(kDegree<T>);
 #pragma unroll
-  for (int i = 6; i >= 0; --i)
+  for (int i = kDegree<T> - 1; i >= 0; --i)
 #pragma unroll
-    for (int k = 0; k < K; ++k) s[k] = f2_fma(s[k], e[k], f2_const(kLog1p[i]));
+    for (int k = 0; k < K; ++k) s[k] = f2_fma(s[k], e[k], log1p_term<T>(i));
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const float2 f = f2_unpack(z[k]);
@@ -183,28 +211,39 @@ __device__ __forceinline__ void softplus_neg(const uint64_t (&z)[K], uint64_t (&
   }
 }
 // e^{-S / tau} - 1 of K pairs by the expansion
-template <int K>
+template <typename T, int K>
 __device__ __forceinline__ void expm1_small(const uint64_t (&s)[K], const DecayParams& g, uint64_t (&r)[K]) {
 #pragma unroll
-  for (int k = 0; k < K; ++k) r[k] = f2_const(g.expm1[4]);
+  for (int k = 0; k < K; ++k) r[k] = f2_const(g.expm1[kExpDegree<T>]);
 #pragma unroll
-  for (int i = 3; i >= 0; --i)
+  for (int i = kExpDegree<T> - 1; i >= 0; --i)
 #pragma unroll
     for (int k = 0; k < K; ++k) r[k] = f2_fma(r[k], s[k], f2_const(g.expm1[i]));
 #pragma unroll
   for (int k = 0; k < K; ++k) r[k] = f2_mul(s[k], r[k]);
 }
+// 1 - sigmoid(z)
+template <typename T>
+__device__ __forceinline__ float sigmoid_down(float z) {
+  const float e = exp_neg_abs<T>(z);
+  return (z >= 0.f ? e : 1.f) * rcp_approx(1.f + e);
+}
 
 // -c of K pairs of logits. With S = softplus(-z), -c = e^{-S / tau} - 1 is S times a polynomial in S
 // while S <= tau / 2; beyond (FAR: look for it), where e^{-S / tau} < 0.61 loses nothing in the
-// difference from one, it is that difference. For f32 tensors the library functions: their
-// callers compare 24 bits, and 12 bytes an element leave time. TAU1: c = 1 - sigmoid(z) in closed form.
+// difference from one, it is that difference. TAU1: c = 1 - sigmoid(z) in closed form.
 template <typename T, bool TAU1, bool FAR, int K>
 __device__ __forceinline__ void neg_decay(const uint64_t (&z)[K], const DecayParams& g, uint64_t (&nc)[K]) {
-  if constexpr (sizeof(T) == 2 && !TAU1) {
+  if constexpr (TAU1) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const float2 f = f2_unpack(z[k]);
+      nc[k] = f2_pack(-sigmoid_down<T>(f.x), -sigmoid_down<T>(f.y));
+    }
+  } else {
     uint64_t s[K];
-    softplus_neg(z, s);
-    expm1_small(s, g, nc);
+    softplus_neg<T>(z, s);
+    expm1_small<T>(s, g, nc);
     if constexpr (FAR) {
 #pragma unroll
       for (int k = 0; k < K; ++k) {
@@ -215,24 +254,6 @@ __device__ __forceinline__ void neg_decay(const uint64_t (&z)[K], const DecayPar
         nc[k] = f2_pack(n.x, n.y);
       }
     }
-  } else {
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const float2 f = f2_unpack(z[k]);
-      float v[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float u = i ? f.y : f.x;
-        if constexpr (sizeof(T) == 4) {
-          const float e = expf(-fabsf(u));
-          v[i] = TAU1 ? -(u >= 0.f ? e : 1.f) / (1.f + e) : expm1f(-(log1pf(e) + fmaxf(-u, 0.f)) * g.inv_tau);
-        } else {
-          const float e = ex2_approx(-kLog2e * fabsf(u));
-          v[i] = -(u >= 0.f ? e : 1.f) * rcp_approx(1.f + e);
-        }
-      }
-      nc[k] = f2_pack(v[0], v[1]);
-    }
   }
 }
 
@@ -241,7 +262,7 @@ __device__ __forceinline__ void neg_decay(const uint64_t (&z)[K], const DecayPar
 template <typename T, bool TAU1, int R>
 __device__ __forceinline__ void row_decays(const typename Pair<T>::Raw* zs, const DecayParams& g, uint64_t (&nc)[R]) {
   using P = Pair<T>;
-  constexpr int K = sizeof(T) == 2 ? 4 : 2;
+  constexpr int K = 4;
   auto rows = [&](auto far) {
 #pragma unroll
     for (int r = 0; r < R; r += K) {
@@ -254,7 +275,7 @@ __device__ __forceinline__ void row_decays(const typename Pair<T>::Raw* zs, cons
     }
   };
   bool far = false;
-  if constexpr (sizeof(T) == 2 && !TAU1) {
+  if constexpr (!TAU1) {
     typename P::Raw least = zs[0];
 #pragma unroll
     for (int r = 1; r < R; ++r) least = P::least(least, zs[r * 32]);
@@ -269,15 +290,7 @@ __device__ __forceinline__ void row_decays(const typename Pair<T>::Raw* zs, cons
 template <typename T>
 __device__ __forceinline__ uint64_t decay_slope(uint64_t z, uint64_t nc, float inv_tau) {
   const float2 f = f2_unpack(z);
-  float2 d;
-  if constexpr (sizeof(T) == 4) {
-    const float e0 = expf(-fabsf(f.x)), e1 = expf(-fabsf(f.y));
-    d = make_float2((f.x >= 0.f ? e0 : 1.f) / (1.f + e0), (f.y >= 0.f ? e1 : 1.f) / (1.f + e1));
-  } else {
-    const float e0 = ex2_approx(-kLog2e * fabsf(f.x)), e1 = ex2_approx(-kLog2e * fabsf(f.y));
-    d = make_float2((f.x >= 0.f ? e0 : 1.f) * rcp_approx(1.f + e0), (f.y >= 0.f ? e1 : 1.f) * rcp_approx(1.f + e1));
-  }
-  return f2_mul(f2_mul(f2_pack(d.x, d.y), f2_both(inv_tau)), f2_add(nc, f2_both(1.f)));
+  return f2_mul(f2_mul(f2_pack(sigmoid_down<T>(f.x), sigmoid_down<T>(f.y)), f2_both(inv_tau)), f2_add(nc, f2_both(1.f)));
 }
 
 // h - c h + u
@@ -427,13 +440,13 @@ __device__ __forceinline__ void put(const uint8_t* from, const Lane<T, VEC>& l, 
 }
 
 // ---------------------------------------------------------------- forward
-constexpr int kWarps = 8;
+constexpr int kWarps = 16;
 constexpr int kForwardStages = 2;  // steps of rows in shared memory: one used, one on its way
 constexpr int kForwardRows = kWarps * kForwardStages * 2 * kRowsBytes;
 constexpr int kSlots = 2 * 32 * sizeof(Join);  // what one block of a cluster sends, double-buffered
 
 template <typename T, bool VEC, bool TAU1, bool TIED>
-__global__ void __launch_bounds__(kWarps * 32, 3) scan_forward_kernel(const ScanParams p) {
+__global__ void __launch_bounds__(kWarps * 32, 1) scan_forward_kernel(const ScanParams p) {
   using P = Pair<T>;
   using Raw = typename P::Raw;
   constexpr int R = kRowsOf<T>, kRows = kWarps * R, kStages = kForwardStages;
@@ -751,7 +764,7 @@ __global__ void __launch_bounds__(kBackRelay * 32, 2) scan_relay_backward_kernel
 constexpr int kBackRows = kWarps * 2 * 3 * kRowsBytes;
 
 template <typename T, bool VEC, bool TAU1, bool TIED>
-__global__ void __launch_bounds__(kWarps * 32, 2) scan_backward_kernel(const ScanParams p) {
+__global__ void __launch_bounds__(kWarps * 32, 1) scan_backward_kernel(const ScanParams p) {
   using P = Pair<T>;
   using Raw = typename P::Raw;
   constexpr int R = kRowsOf<T>;
@@ -904,35 +917,67 @@ bool aligned_rows(const Rows& r, int run, int dtype) {
 }
 bool aligned_state(const float* s) { return reinterpret_cast<uintptr_t>(s) % 8 == 0; }
 
-int multiprocessors() {
-  int dev = 0, n = 148;
-  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-  return n;
+// Clusters of 1 .. kMaxCluster blocks of a split-rows kernel that run at once on the current device
+// (its blocks fill an SM, and a cluster stays inside one of the GPU's SM groups: on a B200 148,
+// 74, .. 33 of 4, .. 15 of 8), asked for once a device.
+const int* clusters_at_once(const void* kernel, int threads, int shared) {
+  constexpr int kDevices = 64;
+  static int table[kDevices][kMaxCluster + 1];
+  static std::once_flag once[kDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) dev = 0;
+  std::call_once(once[dev], [&] {
+    for (int c = 1; c <= kMaxCluster; ++c) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(c);
+      cfg.blockDim = dim3(threads);
+      cfg.dynamicSmemBytes = shared;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = c;
+      attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      int n = 0;
+      if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) n = 1;
+      table[dev][c] = n;
+    }
+  });
+  return table[dev];
 }
 
-// Whether one chain per channel tile and sequence is the form to take, or rows are split.
-bool one_chain(long long tiles, int L) {
-  if (const char* e = getenv("SCAN_CHAIN")) return atoi(e);  // TEMP
-  return tiles >= 96 || L <= 1024;
+// Whether one block per channel tile and sequence is the form to take, or its rows are split over a
+// cluster. A block of the first form keeps its SM busy by itself (9.5 ns a row of 64
+// channels), one of the second at half that rate or more: where two blocks a tile find an
+// SM each they win (8 tiles of 16384 rows: 39 us against 156, 64 tiles with gradients 395
+// against 519), unless the rows are few (256 rows: 5.8 us against 5.3, 1024: 7.4 against 12.7).
+bool one_block(long long tiles, int L, int rows, int pairs) { return tiles > pairs || L <= 2 * rows; }
+
+// Blocks of a cluster: the fewest waves times steps, and of those the fewest blocks.
+int pick_cluster(long long tiles, int L, int rows, const int* at_once) {
+  int best = 1;
+  long long least = 0;
+  for (int c = 1; c <= kMaxCluster; ++c) {
+    const long long time = (tiles + at_once[c] - 1) / at_once[c] * ((L + static_cast<long long>(c) * rows - 1) / (static_cast<long long>(c) * rows));
+    if (c == 1 || time < least) best = c, least = time;
+  }
+  return best;
 }
 
-// Blocks per channel tile where rows are split: enough to give every SM one.
-int pick_cluster(long long tiles, int L, int rows) {
-  int c = 1;
-  while (c < kMaxCluster && tiles * c < multiprocessors() && static_cast<long long>(c) * rows < L) c *= 2;
-  return c;
-}
-
-// (e^{-s} - 1) / s on [0, 1/2]: a Chebyshev expansion cut off at degree 4 (relative error
-// 6e-8), with the powers of 1 / tau in its coefficients.
-DecayParams decay_params(float inv_tau) {
-  const double k[5] = {-0.99999994, 0.4999924, -0.166547343, 0.0409987494, -0.0067685456};
+// (e^{-s} - 1) / s on [0, 1/2]: Chebyshev expansions cut off at degree 4 for 16-bit tensors
+// (relative error 6e-8) and 5 for f32 (1e-9), with the powers of 1 / tau in the coefficients.
+DecayParams decay_params(float inv_tau, int dtype) {
+  constexpr double k4[6] = {-0.99999994, 0.4999924, -0.166547343, 0.0409987494, -0.0067685456, 0};
+  constexpr double k5[6] = {-0.999999998605, 0.499999805417, -0.166662209042, 0.0416289147095, -0.00818699328274, 0.00112132441342};
   DecayParams g;
   g.inv_tau = inv_tau;
   g.far = 0.5f / inv_tau;
   g.far_logit = static_cast<float>(-std::log(std::expm1(0.5 / inv_tau)));  // softplus(-z) = far; -inf for large tau
   double power = inv_tau;
-  for (int i = 0; i < 5; ++i, power *= inv_tau) g.expm1[i] = make_float2(static_cast<float>(k[i] * power), static_cast<float>(k[i] * power));
+  for (int i = 0; i < 6; ++i, power *= inv_tau) {
+    const float v = static_cast<float>((dtype == kF32 ? k5 : k4)[i] * power);
+    g.expm1[i] = make_float2(v, v);
+  }
   return g;
 }
 
@@ -960,7 +1005,7 @@ int scan_saved_rows(int dtype) { return dtype == kF32 ? kRowsOf<float> : kRowsOf
 
 cudaError_t launch_scan_forward(const ScanParams& params, cudaStream_t st) {
   ScanParams p = params;
-  p.gate = decay_params(p.inv_tau);
+  p.gate = decay_params(p.inv_tau, p.dtype);
   const int run = p.dtype == kF32 ? 4 : 8;
   const bool vec = p.D % run == 0 && aligned_rows(p.x, run, p.dtype) && aligned_rows(p.z, run, p.dtype) &&
                    aligned_rows(p.h, run, p.dtype) && aligned_state(p.h0) && aligned_state(p.last) && aligned_state(p.saved);
@@ -969,12 +1014,17 @@ cudaError_t launch_scan_forward(const ScanParams& params, cudaStream_t st) {
   by_kind(p.dtype, vec, p.inv_tau == 1.f, p.tied, [&](auto t, auto v, auto u, auto i) {
     using T = decltype(t);
     constexpr bool V = decltype(v)::value, U = decltype(u)::value, I = decltype(i)::value;
-    if (one_chain(tiles, p.L)) {
+    const auto split = scan_forward_kernel<T, V, U, I>;
+    constexpr int kRowsAtOnce = kWarps * kRowsOf<T>, kShared = kForwardRows + kMaxCluster * kSlots;
+    e = cudaFuncSetAttribute(split, cudaFuncAttributeMaxDynamicSharedMemorySize, kShared);
+    if (e != cudaSuccess) return;
+    const int* at_once = clusters_at_once(reinterpret_cast<const void*>(split), kWarps * 32, kShared);
+    if (one_block(tiles, p.L, kRowsAtOnce, at_once[2])) {
       p.cluster = 1;
       e = launch(scan_relay_kernel<T, V, U, I>, p, kRelay * 32, kRelayShared, st);
     } else {
-      p.cluster = pick_cluster(tiles, p.L, kWarps * kRowsOf<T>);
-      e = launch(scan_forward_kernel<T, V, U, I>, p, kWarps * 32, kForwardRows + (p.cluster > 1 ? p.cluster * kSlots : 0), st);
+      p.cluster = pick_cluster(tiles, p.L, kRowsAtOnce, at_once);
+      e = launch(split, p, kWarps * 32, kShared, st);
     }
   });
   return e;
@@ -982,7 +1032,7 @@ cudaError_t launch_scan_forward(const ScanParams& params, cudaStream_t st) {
 
 cudaError_t launch_scan_backward(const ScanParams& params, cudaStream_t st) {
   ScanParams p = params;
-  p.gate = decay_params(p.inv_tau);
+  p.gate = decay_params(p.inv_tau, p.dtype);
   const int run = p.dtype == kF32 ? 4 : 8;
   const bool vec = p.D % run == 0 && aligned_rows(p.x, run, p.dtype) && aligned_rows(p.z, run, p.dtype) &&
                    aligned_rows(p.dh, run, p.dtype) && aligned_rows(p.dx, run, p.dtype) &&
@@ -993,12 +1043,17 @@ cudaError_t launch_scan_backward(const ScanParams& params, cudaStream_t st) {
   by_kind(p.dtype, vec, p.inv_tau == 1.f, p.tied, [&](auto t, auto v, auto u, auto i) {
     using T = decltype(t);
     constexpr bool V = decltype(v)::value, U = decltype(u)::value, I = decltype(i)::value;
-    if (one_chain(tiles, p.L)) {
+    const auto split = scan_backward_kernel<T, V, U, I>;
+    constexpr int kRowsAtOnce = kWarps * kRowsOf<T>, kShared = kBackRows + kMaxCluster * kSlots;
+    e = cudaFuncSetAttribute(split, cudaFuncAttributeMaxDynamicSharedMemorySize, kShared);
+    if (e != cudaSuccess) return;
+    const int* at_once = clusters_at_once(reinterpret_cast<const void*>(split), kWarps * 32, kShared);
+    if (one_block(tiles, p.L, kRowsAtOnce, at_once[2])) {
       p.cluster = 1;
       e = launch(scan_relay_backward_kernel<T, V, U, I>, p, kBackRelay * 32, kBackRelayShared, st);
     } else {
-      p.cluster = pick_cluster(tiles, p.L, kWarps * kRowsOf<T>);
-      e = launch(scan_backward_kernel<T, V, U, I>, p, kWarps * 32, kBackRows + (p.cluster > 1 ? p.cluster * kSlots : 0), st);
+      p.cluster = pick_cluster(tiles, p.L, kRowsAtOnce, at_once);
+      e = launch(split, p, kWarps * 32, kShared, st);
     }
   });
   return e;
@@ -1006,7 +1061,7 @@ cudaError_t launch_scan_backward(const ScanParams& params, cudaStream_t st) {
 
 cudaError_t launch_scan_step(const StepParams& params, cudaStream_t st) {
   StepParams p = params;
-  p.gate = decay_params(p.inv_tau);
+  p.gate = decay_params(p.inv_tau, p.dtype);
   const Rows rows[3] = {{const_cast<void*>(p.x), p.x_row, 0}, {const_cast<void*>(p.z), p.z_row, 0}, {p.h, p.h_row, 0}};
   bool vec = p.D % 2 == 0 && aligned_state(p.state);
   for (const Rows& r : rows) vec = vec && aligned_rows(r, 2, p.dtype);

@@ -27,7 +27,7 @@ int scan_saved_rows(int dtype);  // rows between two saved states
 // packed operand.
 struct DecayParams {
   float inv_tau, far, far_logit;
-  float2 expm1[5];
+  float2 expm1[6];
 };
 
 struct ScanParams {
