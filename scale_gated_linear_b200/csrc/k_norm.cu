@@ -1034,10 +1034,12 @@ cudaError_t launch_norm_backward(const NormParams& p, cudaStream_t st) {
       const RowPlan q = row_plan(p, v, kRowBlocksBackward);
       const int sums = (q.rpi - 1) * q.gs * (p.C / p.G) * 8;
       by_vectors<V>(p, q, [&](auto nv, auto team) {
-        auto kernel = norm_rows_backward_kernel<T, V, decltype(nv)::value, decltype(team)::value>;
-        const int rows = kAhead * kRowStage<T, V, decltype(nv)::value>, shared = rows > sums ? rows : sums;
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, shared);
-        if (e == cudaSuccess) kernel<<<dim3(q.slices, q.blocks), kThreads, shared, st>>>(p, q);
+        constexpr auto kernel = norm_rows_backward_kernel<T, V, decltype(nv)::value, decltype(team)::value>;
+        // a block's sums need at most 8 bytes for each of its threads' values
+        constexpr int kRows = kAhead * kRowStage<T, V, decltype(nv)::value>, kSums = kThreads * V * decltype(nv)::value * 8;
+        constexpr int kShared = kRows > kSums ? kRows : kSums;
+        e = allow_shared<kernel>(kShared);
+        if (e == cudaSuccess) kernel<<<dim3(q.slices, q.blocks), kThreads, kRows > sums ? kRows : sums, st>>>(p, q);
       });
       if (e == cudaSuccess) launch_weights(p, static_cast<const float*>(p.workspace), q.blocks, st);
     } else {

@@ -981,9 +981,9 @@ DecayParams decay_params(float inv_tau, int dtype) {
   return g;
 }
 
-template <typename K>
-cudaError_t launch(K kernel, const ScanParams& p, int threads, int shared, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, shared);
+template <auto kernel>
+cudaError_t launch(const ScanParams& p, int threads, int shared, cudaStream_t st) {
+  const cudaError_t e = allow_shared<kernel>(shared);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((p.D + 63) / 64 * p.cluster, p.B);
@@ -1014,17 +1014,16 @@ cudaError_t launch_scan_forward(const ScanParams& params, cudaStream_t st) {
   by_kind(p.dtype, vec, p.inv_tau == 1.f, p.tied, [&](auto t, auto v, auto u, auto i) {
     using T = decltype(t);
     constexpr bool V = decltype(v)::value, U = decltype(u)::value, I = decltype(i)::value;
-    const auto split = scan_forward_kernel<T, V, U, I>;
     constexpr int kRowsAtOnce = kWarps * kRowsOf<T>, kShared = kForwardRows + kMaxCluster * kSlots;
-    e = cudaFuncSetAttribute(split, cudaFuncAttributeMaxDynamicSharedMemorySize, kShared);
+    e = allow_shared<scan_forward_kernel<T, V, U, I>>(kShared);
     if (e != cudaSuccess) return;
-    const int* at_once = clusters_at_once(reinterpret_cast<const void*>(split), kWarps * 32, kShared);
+    const int* at_once = clusters_at_once(reinterpret_cast<const void*>(scan_forward_kernel<T, V, U, I>), kWarps * 32, kShared);
     if (one_block(tiles, p.L, kRowsAtOnce, at_once[2])) {
       p.cluster = 1;
-      e = launch(scan_relay_kernel<T, V, U, I>, p, kRelay * 32, kRelayShared, st);
+      e = launch<scan_relay_kernel<T, V, U, I>>(p, kRelay * 32, kRelayShared, st);
     } else {
       p.cluster = pick_cluster(tiles, p.L, kRowsAtOnce, at_once);
-      e = launch(split, p, kWarps * 32, kShared, st);
+      e = launch<scan_forward_kernel<T, V, U, I>>(p, kWarps * 32, kShared, st);
     }
   });
   return e;
@@ -1043,17 +1042,16 @@ cudaError_t launch_scan_backward(const ScanParams& params, cudaStream_t st) {
   by_kind(p.dtype, vec, p.inv_tau == 1.f, p.tied, [&](auto t, auto v, auto u, auto i) {
     using T = decltype(t);
     constexpr bool V = decltype(v)::value, U = decltype(u)::value, I = decltype(i)::value;
-    const auto split = scan_backward_kernel<T, V, U, I>;
     constexpr int kRowsAtOnce = kWarps * kRowsOf<T>, kShared = kBackRows + kMaxCluster * kSlots;
-    e = cudaFuncSetAttribute(split, cudaFuncAttributeMaxDynamicSharedMemorySize, kShared);
+    e = allow_shared<scan_backward_kernel<T, V, U, I>>(kShared);
     if (e != cudaSuccess) return;
-    const int* at_once = clusters_at_once(reinterpret_cast<const void*>(split), kWarps * 32, kShared);
+    const int* at_once = clusters_at_once(reinterpret_cast<const void*>(scan_backward_kernel<T, V, U, I>), kWarps * 32, kShared);
     if (one_block(tiles, p.L, kRowsAtOnce, at_once[2])) {
       p.cluster = 1;
-      e = launch(scan_relay_backward_kernel<T, V, U, I>, p, kBackRelay * 32, kBackRelayShared, st);
+      e = launch<scan_relay_backward_kernel<T, V, U, I>>(p, kBackRelay * 32, kBackRelayShared, st);
     } else {
       p.cluster = pick_cluster(tiles, p.L, kRowsAtOnce, at_once);
-      e = launch(split, p, kWarps * 32, kShared, st);
+      e = launch<scan_backward_kernel<T, V, U, I>>(p, kWarps * 32, kShared, st);
     }
   });
   return e;

@@ -11,14 +11,17 @@ using namespace msgla;
 
 namespace {
 
+// Makes `dev` the current device for a call, and the previous one again.
 struct Device {
   int prev = -1;
-  bool ok = false;
+  bool ok = false, moved = false;
   explicit Device(int dev) {
-    if (cudaGetDevice(&prev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess) ok = true;
+    if (cudaGetDevice(&prev) != cudaSuccess) return;
+    moved = prev != dev;
+    ok = !moved || cudaSetDevice(dev) == cudaSuccess;
   }
   ~Device() {
-    if (prev >= 0) cudaSetDevice(prev);
+    if (moved) cudaSetDevice(prev);
   }
 };
 

@@ -2,6 +2,7 @@
 // recurrence (k_scan.cu), group normalisation (k_norm.cu) and their C entry
 // points (ops_abi.cu). Not part of the public interface.
 #pragma once
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -73,6 +74,21 @@ struct NormParams {
 size_t norm_workspace(const NormParams& p, bool backward);
 cudaError_t launch_norm_forward(const NormParams& p, cudaStream_t st);
 cudaError_t launch_norm_backward(const NormParams& p, cudaStream_t st);
+
+// Lets `kernel` use `bytes` of dynamic shared memory on the current device; asked of the driver once
+// for each kernel (a template argument, so each has its own mark) and device.
+template <auto kernel>
+cudaError_t allow_shared(int bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 // ---------------------------------------------------------------- element types
 enum : int { kBF16 = 0, kF16 = 1, kF32 = 2 };

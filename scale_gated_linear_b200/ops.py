@@ -54,15 +54,16 @@ def _norm_config(device: int, dtype, C: int, groups: int, activation, center: bo
 
 
 def _check_x(name: str, t, dims: int):
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in _DTYPES and t.dim() == dims:
+        return
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         _refuse(f"{name} must be a cuda tensor")
     if t.dtype not in _DTYPES:
         _refuse(f"{name} has dtype {t.dtype}: bfloat16, float16 or float32", -2)
-    if t.dim() != dims:
-        _refuse(f"{name} has {t.dim()} dimensions, {dims} are needed")
+    _refuse(f"{name} has {t.dim()} dimensions, {dims} are needed")
 
 
-def _check_like(name: str, t, x, contiguous: bool = False):
+def _check_like(name: str, t, x):
     if not isinstance(t, torch.Tensor) or t.shape != x.shape or t.dtype != x.dtype or t.device != x.device:
         _refuse(f"{name} must have the shape {tuple(x.shape)}, the dtype {x.dtype} and the device {x.device}")
 
@@ -102,30 +103,51 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-class _On:
-    """The stream of a call: outputs are allocated for it, and inputs that the caller may
-    free are kept from other streams until it has used them."""
+# The handle of torch's current stream; a Stream object would take 2 us to make.
+_current_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
-    def __init__(self, device, stream, *inputs):
-        current = torch.cuda.current_stream(device)
-        self.stream = current if stream is None else stream
-        self.other = self.stream.cuda_stream != current.cuda_stream
-        if self.other:
-            if self.stream.device != device:
-                _refuse(f"the stream is on {self.stream.device}, the tensors are on {device}")
+
+class _On:
+    """The stream of a call that named one: outputs are allocated for it, and inputs that the
+    caller may free are kept from other streams until it has used them."""
+
+    def __init__(self, device, stream, inputs):
+        if stream.device != device:
+            _refuse(f"the stream is on {stream.device}, the tensors are on {device}")
+        self.stream, self.handle = stream, stream.cuda_stream
+        if self.handle != _current_handle(device.index):
             for t in inputs:
                 if t is not None:
-                    t.record_stream(self.stream)
+                    t.record_stream(stream)
 
-    @property
-    def handle(self):
-        return ctypes.c_void_p(self.stream.cuda_stream)
+    def empty_like(self, t):
+        with torch.cuda.stream(self.stream):
+            return torch.empty_like(t, memory_format=torch.contiguous_format)
 
     def empty(self, shape, dtype, device):
-        if not self.other:
-            return torch.empty(shape, dtype=dtype, device=device)
         with torch.cuda.stream(self.stream):
             return torch.empty(shape, dtype=dtype, device=device)
+
+
+class _Current:
+    """A call on torch's current stream of its device."""
+    __slots__ = ("handle",)
+
+    def __init__(self, index):
+        self.handle = _current_handle(index)
+
+    @staticmethod
+    def empty_like(t):
+        return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+    @staticmethod
+    def empty(shape, dtype, device):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _on(device, stream, *inputs):
+    return _Current(device.index) if stream is None else _On(device, stream, inputs)
 
 
 def _check_out(out, x):
@@ -162,9 +184,9 @@ def _scan_forward(x, gate, mask, initial_state, gate_normalizer, tied, save, out
     B, L, D = x.shape
     if initial_state is not None:
         _check_f32("initial_state", initial_state, (B, D), x.device)
-    on = _On(x.device, stream, x, gate, mask, initial_state, out)
+    on = _on(x.device, stream, x, gate, mask, initial_state, out)
     if out is None:
-        out = on.empty((B, L, D), x.dtype, x.device)
+        out = on.empty_like(x)
     else:
         _check_out(out, x)
     last = on.empty((B, D), torch.float32, x.device)
@@ -194,8 +216,8 @@ def gated_scan_backward(dh, dlast, saved: ScanSaved, *, stream=None):
         _check_like("dh", dh, x)
     if dlast is not None:
         _check_f32("dlast", dlast, (B, D), x.device)
-    on = _On(x.device, stream, x, gate, mask, states, dh, dlast)
-    dx, dgate = on.empty((B, L, D), x.dtype, x.device), on.empty((B, L, D), x.dtype, x.device)
+    on = _on(x.device, stream, x, gate, mask, states, dh, dlast)
+    dx, dgate = on.empty_like(x), on.empty_like(x)
     dstate = on.empty((B, D), torch.float32, x.device) if has_state else None
     _lib.check(_lib.load().msgla_scan_backward(cfg, B, L, _rows3("x", x), _rows3("gate", gate), _ptr(mask),
                                                states.data_ptr(), None if dh is None else _rows3("dh", dh),
@@ -281,9 +303,9 @@ def gated_scan_step(x, gate, state, *, mask=None, gate_normalizer: float = 16.0,
     _check_f32("state", state, (B, D), x.device)
     if torch.is_grad_enabled() and (x.requires_grad or gate.requires_grad or state.requires_grad):
         _refuse("gated_scan_step has no gradients: call it under torch.no_grad()", -2)
-    on = _On(x.device, stream, x, gate, mask, state, out)
+    on = _on(x.device, stream, x, gate, mask, state, out)
     if out is None:
-        out = on.empty((B, D), x.dtype, x.device)
+        out = on.empty_like(x)
     else:
         _check_out(out, x)
     _lib.check(_lib.load().msgla_scan_step(cfg, B, _rows2("x", x), _rows2("gate", gate), _ptr(mask), state.data_ptr(),
@@ -324,9 +346,9 @@ def _norm_forward(x, groups, weight, bias, gate, mask, activation, eps, center, 
         mask = _check_mask(mask, x.shape[:-1], x.device)
     cfg = _norm_config(x.device.index, x.dtype, C, groups, activation, bool(center), float(eps))
     N, S = x.shape[0], 1 if x.dim() == 2 else x.shape[1]
-    on = _On(x.device, stream, x, weight, bias, gate, mask, out)
+    on = _on(x.device, stream, x, weight, bias, gate, mask, out)
     if out is None:
-        out = on.empty(x.shape, x.dtype, x.device)
+        out = on.empty_like(x)
     else:
         _check_out(out, x)
     stats = on.empty((N, groups, 2), torch.float32, x.device) if save else None
@@ -337,10 +359,17 @@ def _norm_forward(x, groups, weight, bias, gate, mask, activation, eps, center, 
     return out, (NormSaved(x, gate, weight, bias, mask, stats, cfg) if save else None)
 
 
-def _norm_workspace(cfg, N, S, gradients, on, device):
+@functools.lru_cache(maxsize=1024)
+def _norm_workspace_bytes(dtype: int, C: int, groups: int, N: int, S: int, gradients: int, device: int):
     n = ctypes.c_size_t()
-    _lib.check(_lib.load().msgla_group_norm_workspace_size(cfg, N, S, 1 if gradients else 0, ctypes.byref(n)))
-    return (on.empty((n.value,), torch.uint8, device) if n.value else None), n.value
+    cfg = _lib.NormConfig(device, dtype, C, groups, 0, 1, 1.0)
+    _lib.check(_lib.load().msgla_group_norm_workspace_size(cfg, N, S, gradients, ctypes.byref(n)))
+    return n.value
+
+
+def _norm_workspace(cfg, N, S, gradients, on, device):
+    n = _norm_workspace_bytes(cfg.dtype, cfg.C, cfg.groups, N, S, 1 if gradients else 0, cfg.device)
+    return (on.empty((n,), torch.uint8, device) if n else None), n
 
 
 def group_norm_forward(x, groups: int, weight=None, bias=None, *, gate=None, mask=None, activation="none",
@@ -356,9 +385,9 @@ def group_norm_backward(dy, saved: NormSaved, *, stream=None):
     x, gate, weight, bias, mask, stats, cfg = saved
     _check_like("dy", dy, x)
     N, S = x.shape[0], 1 if x.dim() == 2 else x.shape[1]
-    on = _On(x.device, stream, x, gate, weight, bias, mask, stats, dy)
-    dx = on.empty(x.shape, x.dtype, x.device)
-    dgate = None if gate is None else on.empty(x.shape, x.dtype, x.device)
+    on = _on(x.device, stream, x, gate, weight, bias, mask, stats, dy)
+    dx = on.empty_like(x)
+    dgate = None if gate is None else on.empty_like(x)
     dw = None if weight is None else on.empty((cfg.C,), torch.float32, x.device)
     db = None if bias is None else on.empty((cfg.C,), torch.float32, x.device)
     ws, nbytes = _norm_workspace(cfg, N, S, True, on, x.device)
