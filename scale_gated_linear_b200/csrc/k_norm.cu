@@ -332,6 +332,7 @@ constexpr int kRowStage = kThreads * NV * 3 * (V == 1 ? 4 : 16);  // bytes of a 
 template <typename T, int V, int NV, int TEAM>
 __global__ void __launch_bounds__(kThreads, V * NV <= 16 ? 2 : 1) norm_rows_backward_kernel(const NormParams p, const RowPlan q) {
   __shared__ float part[2][2][kThreads / 32];
+  griddep_launch();
   extern __shared__ __align__(16) uint8_t dynamic[];  // rows; in the end [rpi - 1][gs * cg][2] sums
   constexpr bool kKeep = V * NV <= 16;  // weights in registers
   int turn = 0;
@@ -483,6 +484,7 @@ __global__ void __launch_bounds__(kThreads, V * NV <= 16 ? 2 : 1) norm_rows_back
 // dw and db from `rows` partial sums [rows][2][C]. 32 channels a block.
 __global__ void __launch_bounds__(1024) norm_weights_kernel(const NormParams p, const float* part, int rows) {
   __shared__ float2 sums[32][33];
+  griddep_wait();
   const int c = blockIdx.x * 32 + threadIdx.x;
   float2 s = make_float2(0.f, 0.f);
   if (c < p.C)
@@ -543,6 +545,7 @@ template <typename T, int V>
 __global__ void __launch_bounds__(kThreads) norm_sums_kernel(const NormParams p, const BlockPlan q, float2* seg, float* rows_of) {
   __shared__ float2 cell[kThreads];  // a thread's V channels: mean and squares
   __shared__ int counts[kThreads];
+  griddep_launch();
   const Part part(q);
   const int tx = threadIdx.x % q.tx, ty = threadIdx.x / q.tx, c = part.tile * q.width + tx * V, cg = p.C / p.G;
   const long long s0 = static_cast<long long>(part.chunk) * q.rows, s1 = min(s0 + q.rows, p.S);
@@ -556,12 +559,14 @@ __global__ void __launch_bounds__(kThreads) norm_sums_kernel(const NormParams p,
       while (s < s1 && m && !m[s]) s += q.ty;
       if (s < s1) first = to_f32(x[s * p.x.row]);
     }
+    uint32_t next = rows_valid(m, s, s1, q.ty);
     for (; s < s1; s += kUnroll * q.ty) {
-      const uint32_t bits = rows_valid(m, s, s1, q.ty);
+      const uint32_t bits = next;
       Vec<T, V> v[kUnroll];
 #pragma unroll
       for (int k = 0; k < kUnroll; ++k)
         if (bits >> k & 1) v[k] = load<T, V>(x + (s + k * q.ty) * p.x.row);
+      next = rows_valid(m, s + kUnroll * q.ty, s1, q.ty);
 #pragma unroll
       for (int k = 0; k < kUnroll; ++k)
         if (bits >> k & 1) {
@@ -653,9 +658,11 @@ template <typename T, int V>
 __global__ void __launch_bounds__(kThreads, 3) norm_apply_kernel(const NormParams p, const BlockPlan q, const float2* seg,
                                                               const float* rows_of) {
   extern __shared__ float2 stat[];  // groups that meet the tile
+  griddep_launch();
   const Part part(q);
   const int tx = threadIdx.x % q.tx, ty = threadIdx.x / q.tx, c = part.tile * q.width + tx * V, cg = p.C / p.G;
   const int t0 = part.tile * q.width, t1 = min(t0 + q.width, p.C), g0 = t0 / cg;
+  griddep_wait();
   for (int g = g0 + warp_id(); g * cg < t1; g += kThreads / 32) {
     const float2 v = join_stats(p, q, part.n, g, seg, rows_of);
     if (lane_id() == 0) {
@@ -677,8 +684,9 @@ __global__ void __launch_bounds__(kThreads, 3) norm_apply_kernel(const NormParam
   const T* gp = at<T>(p.gate, part.n, 0, c);
   T* yp = at<T>(p.y, part.n, 0, c);
   by_act(p.act, p.gate.ptr, [&](auto kind, auto gated) {
+    uint32_t next = rows_valid(m, s0 + ty, s1, q.ty);
     for (long long s = s0 + ty; s < s1; s += kUnroll * q.ty) {
-      const uint32_t bits = rows_valid(m, s, s1, q.ty);
+      const uint32_t bits = next;
       Vec<T, V> x[kUnroll], gt[kUnroll];
 #pragma unroll
       for (int k = 0; k < kUnroll; ++k)
@@ -686,6 +694,7 @@ __global__ void __launch_bounds__(kThreads, 3) norm_apply_kernel(const NormParam
           x[k] = load<T, V>(xp + (s + k * q.ty) * p.x.row);
           if (gated) gt[k] = load<T, V>(gp + (s + k * q.ty) * p.gate.row);
         }
+      next = rows_valid(m, s + kUnroll * q.ty, s1, q.ty);
 #pragma unroll
       for (int k = 0; k < kUnroll; ++k) {
         Vec<T, V> y = zeros<T, V>();
@@ -713,6 +722,7 @@ __global__ void __launch_bounds__(kThreads, 2) norm_grad_sums_kernel(const NormP
                                                                   float* rows_of) {
   extern __shared__ float2 cell[];  // [ty][width]
   __shared__ int counts[kThreads];
+  griddep_launch();
   const Part part(q);
   const int tx = threadIdx.x % q.tx, ty = threadIdx.x / q.tx, c = part.tile * q.width + tx * V, cg = p.C / p.G;
   const long long s0 = static_cast<long long>(part.chunk) * q.rows, s1 = min(s0 + q.rows, p.S);
@@ -728,8 +738,9 @@ __global__ void __launch_bounds__(kThreads, 2) norm_grad_sums_kernel(const NormP
     const T* dp = at<T>(p.dy, part.n, 0, c);
     const T* gp = at<T>(p.gate, part.n, 0, c);
     by_act(p.act, p.gate.ptr, [&](auto kind, auto gated) {
+      uint32_t next = rows_valid(m, s0 + ty, s1, q.ty);
       for (long long s = s0 + ty; s < s1; s += kUnroll * q.ty) {
-        const uint32_t bits = rows_valid(m, s, s1, q.ty);
+        const uint32_t bits = next;
         count += __popc(bits);
         Vec<T, V> x[kUnroll], d[kUnroll], gt[kUnroll];
 #pragma unroll
@@ -739,6 +750,7 @@ __global__ void __launch_bounds__(kThreads, 2) norm_grad_sums_kernel(const NormP
             d[k] = load<T, V>(dp + (s + k * q.ty) * p.dy.row);
             if (gated) gt[k] = load<T, V>(gp + (s + k * q.ty) * p.gate.row);
           }
+        next = rows_valid(m, s + kUnroll * q.ty, s1, q.ty);
 #pragma unroll
         for (int k = 0; k < kUnroll; ++k)
           if (bits >> k & 1) {
@@ -798,9 +810,11 @@ template <typename T, int V>
 __global__ void __launch_bounds__(kThreads, 2) norm_grad_apply_kernel(const NormParams p, const BlockPlan q, const float2* seg,
                                                                    const float* rows_of) {
   extern __shared__ float2 stat[];  // <dv w>, <dv w xhat> of the groups that meet the tile
+  griddep_launch();
   const Part part(q);
   const int tx = threadIdx.x % q.tx, ty = threadIdx.x / q.tx, c = part.tile * q.width + tx * V, cg = p.C / p.G;
   const int t0 = part.tile * q.width, t1 = min(t0 + q.width, p.C), g0 = t0 / cg;
+  griddep_wait();
   for (int g = g0 + warp_id(); g * cg < t1; g += kThreads / 32) {
     const int a = g * cg, first = a / q.width, segs = (a + cg - 1) / q.width - first + 1;
     float s1v = 0.f, s2v = 0.f, count = 0.f;
@@ -830,8 +844,9 @@ __global__ void __launch_bounds__(kThreads, 2) norm_grad_apply_kernel(const Norm
   T* ox = at<T>(p.dx, part.n, 0, c);
   T* og = at<T>(p.dgate, part.n, 0, c);
   by_act(p.act, p.gate.ptr, [&](auto kind, auto gated) {
+    uint32_t next = rows_valid(m, s0 + ty, s1, q.ty);
     for (long long s = s0 + ty; s < s1; s += kUnroll * q.ty) {
-      const uint32_t bits = rows_valid(m, s, s1, q.ty);
+      const uint32_t bits = next;
       Vec<T, V> x[kUnroll], d[kUnroll], gt[kUnroll];
 #pragma unroll
       for (int k = 0; k < kUnroll; ++k)
@@ -840,6 +855,7 @@ __global__ void __launch_bounds__(kThreads, 2) norm_grad_apply_kernel(const Norm
           d[k] = load<T, V>(dp + (s + k * q.ty) * p.dy.row);
           if (gated) gt[k] = load<T, V>(gp + (s + k * q.ty) * p.gate.row);
         }
+      next = rows_valid(m, s + kUnroll * q.ty, s1, q.ty);
 #pragma unroll
       for (int k = 0; k < kUnroll; ++k) {
         Vec<T, V> dx = zeros<T, V>(), dgate = dx;
@@ -909,8 +925,9 @@ RowPlan row_plan(const NormParams& p, int v, int per_sm) {
 }
 
 // Rows and channels of a block: as many rows at once as there are, up to 32, and chunks so that a
-// thread sums at most 64 rows and the GPU has several blocks an SM.
-BlockPlan block_plan(const NormParams& p, int v) {
+// thread sums at most 64 rows and the blocks fill the SMs' places once (a second wave that is half
+// empty cost a third of the time at 8 x 2048 x 1024).
+BlockPlan block_plan(const NormParams& p, int v, int per_sm) {
   BlockPlan q;
   q.ty = 1;
   while (q.ty < 32 && q.ty < p.S) q.ty *= 2;
@@ -919,7 +936,7 @@ BlockPlan block_plan(const NormParams& p, int v) {
   q.width = q.tx * v;
   q.tiles = (p.C + q.width - 1) / q.width;
   const long long blocks = p.N * q.tiles, rows_at_once = (p.S + q.ty - 1) / q.ty;
-  long long chunks = (4LL * multiprocessors() + blocks - 1) / blocks;
+  long long chunks = static_cast<long long>(per_sm) * multiprocessors() / blocks;
   const long long least = (rows_at_once + 63) / 64, most = rows_at_once < 512 ? rows_at_once : 512;
   if (chunks < least) chunks = least;
   if (chunks > most) chunks = most;
@@ -975,9 +992,29 @@ void by_vectors(const NormParams& p, const RowPlan& q, F&& f) {
 }
 
 constexpr int kRowBlocks = 3, kRowBlocksBackward = 2;  // blocks an SM of the rows form
+constexpr int kBlocks = 3, kBlocksBackward = 2;         // and of the block form
 
-void launch_weights(const NormParams& p, const float* part, int rows, cudaStream_t st) {
-  if (p.dw || p.db) norm_weights_kernel<<<(p.C + 31) / 32, dim3(32, 32), 0, st>>>(p, part, rows);
+// Launches a kernel that may start while its predecessor drains: it waits (griddep_wait) before it
+// reads what that one wrote.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_after(void (*kernel)(KArgs...), dim3 grid, dim3 block, int shared, cudaStream_t st, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = shared;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, KArgs(args)...);
+}
+
+cudaError_t launch_weights(const NormParams& p, const float* part, int rows, cudaStream_t st) {
+  cudaError_t e = cudaSuccess;
+  if (p.dw || p.db) e = launch_after(norm_weights_kernel, dim3((p.C + 31) / 32), dim3(32, 32), 0, st, p, part, rows);
+  return e;
 }
 
 }  // namespace
@@ -991,7 +1028,7 @@ size_t norm_workspace(const NormParams& p, bool backward) {
     if (rows_form(p, v)) {
       n = backward ? static_cast<size_t>(row_plan(p, v, kRowBlocksBackward).blocks) * 2 * p.C * 4 : 0;
     } else {
-      n = BlockSpace(p, block_plan(p, v), backward).bytes;
+      n = BlockSpace(p, block_plan(p, v, backward ? kBlocksBackward : kBlocks), backward).bytes;
     }
     most = n > most ? n : most;
   }
@@ -1010,7 +1047,7 @@ cudaError_t launch_norm_forward(const NormParams& p, cudaStream_t st) {
         norm_rows_forward_kernel<T, V, decltype(nv)::value, decltype(team)::value><<<dim3(q.slices, q.blocks), kThreads, 0, st>>>(p, q);
       });
     } else {
-      const BlockPlan q = block_plan(p, v);
+      const BlockPlan q = block_plan(p, v, kBlocks);
       const BlockSpace s(p, q, false);
       const long long grid = p.N * q.chunks * q.tiles;
       if (grid > 0x7fffffffLL) {
@@ -1018,7 +1055,8 @@ cudaError_t launch_norm_forward(const NormParams& p, cudaStream_t st) {
         return;
       }
       norm_sums_kernel<T, V><<<unsigned(grid), kThreads, 0, st>>>(p, q, s.seg, s.rows_of);
-      norm_apply_kernel<T, V><<<unsigned(grid), kThreads, (q.width + 1) * 8, st>>>(p, q, s.seg, s.rows_of);
+      e = launch_after(norm_apply_kernel<T, V>, dim3(unsigned(grid)), dim3(kThreads), (q.width + 1) * 8, st, p, q,
+                       static_cast<const float2*>(s.seg), static_cast<const float*>(s.rows_of));
     }
   });
   return e == cudaSuccess ? cudaGetLastError() : e;
@@ -1041,9 +1079,9 @@ cudaError_t launch_norm_backward(const NormParams& p, cudaStream_t st) {
         e = allow_shared<kernel>(kShared);
         if (e == cudaSuccess) kernel<<<dim3(q.slices, q.blocks), kThreads, kRows > sums ? kRows : sums, st>>>(p, q);
       });
-      if (e == cudaSuccess) launch_weights(p, static_cast<const float*>(p.workspace), q.blocks, st);
+      if (e == cudaSuccess) e = launch_weights(p, static_cast<const float*>(p.workspace), q.blocks, st);
     } else {
-      const BlockPlan q = block_plan(p, v);
+      const BlockPlan q = block_plan(p, v, kBlocksBackward);
       const BlockSpace s(p, q, true);
       const long long grid = p.N * q.chunks * q.tiles, parts = p.N * q.chunks;
       if (grid > 0x7fffffffLL) {
@@ -1051,8 +1089,9 @@ cudaError_t launch_norm_backward(const NormParams& p, cudaStream_t st) {
         return;
       }
       norm_grad_sums_kernel<T, V><<<unsigned(grid), kThreads, kThreads * V * 8, st>>>(p, q, s.chan, s.seg, s.rows_of);
-      norm_grad_apply_kernel<T, V><<<unsigned(grid), kThreads, (q.width + 1) * 8, st>>>(p, q, s.seg, s.rows_of);
-      launch_weights(p, s.chan, static_cast<int>(parts), st);
+      e = launch_after(norm_grad_apply_kernel<T, V>, dim3(unsigned(grid)), dim3(kThreads), (q.width + 1) * 8, st, p, q,
+                       static_cast<const float2*>(s.seg), static_cast<const float*>(s.rows_of));
+      if (e == cudaSuccess) e = launch_weights(p, s.chan, static_cast<int>(parts), st);
     }
   });
   return e == cudaSuccess ? cudaGetLastError() : e;

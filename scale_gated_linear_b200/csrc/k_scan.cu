@@ -188,11 +188,10 @@ __device__ __forceinline__ float exp_neg_abs(float z) {
   const float lo = fmaf(-kLog2eLow, fabsf(z), fmaf(-kLog2e, fabsf(z), -hi)), e = ex2_approx(hi);
   return hi > -126.f ? fmaf(e, lo * kLn2, e) : e;  // also keeps inf - inf out
 }
-// softplus(-z) of K pairs. The K are taken through every operation together: one pair's
+// softplus(-z) and e^{-|z|} of K pairs. The K are taken through every operation together: one pair's
 // operations wait for each other, and a scheduler has few warps to fill the gaps.
 template <typename T, int K>
-__device__ __forceinline__ void softplus_neg(const uint64_t (&z)[K], uint64_t (&s)[K]) {
-  uint64_t e[K];
+__device__ __forceinline__ void softplus_neg(const uint64_t (&z)[K], uint64_t (&s)[K], uint64_t (&e)[K]) {
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const float2 f = f2_unpack(z[k]);
@@ -222,27 +221,31 @@ __device__ __forceinline__ void expm1_small(const uint64_t (&s)[K], const DecayP
 #pragma unroll
   for (int k = 0; k < K; ++k) r[k] = f2_mul(s[k], r[k]);
 }
-// 1 - sigmoid(z)
-template <typename T>
-__device__ __forceinline__ float sigmoid_down(float z) {
-  const float e = exp_neg_abs<T>(z);
-  return (z >= 0.f ? e : 1.f) * rcp_approx(1.f + e);
+// 1 - sigmoid(z), given e = e^{-|z|}
+__device__ __forceinline__ uint64_t sigmoid_down(uint64_t z, uint64_t e) {
+  const float2 f = f2_unpack(z), g = f2_unpack(e);
+  return f2_pack((f.x >= 0.f ? g.x : 1.f) * rcp_approx(1.f + g.x), (f.y >= 0.f ? g.y : 1.f) * rcp_approx(1.f + g.y));
 }
 
 // -c of K pairs of logits. With S = softplus(-z), -c = e^{-S / tau} - 1 is S times a polynomial in S
 // while S <= tau / 2; beyond (FAR: look for it), where e^{-S / tau} < 0.61 loses nothing in the
 // difference from one, it is that difference. TAU1: c = 1 - sigmoid(z) in closed form.
-template <typename T, bool TAU1, bool FAR, int K>
-__device__ __forceinline__ void neg_decay(const uint64_t (&z)[K], const DecayParams& g, uint64_t (&nc)[K]) {
+// SLOPE: also -dc/dz = a (1 - sigmoid(z)) / tau; for padded rows (z = +inf) both are zero.
+template <typename T, bool TAU1, bool FAR, bool SLOPE, int K>
+__device__ __forceinline__ void neg_decay(const uint64_t (&z)[K], const DecayParams& g, uint64_t (&nc)[K], uint64_t (&slope)[K]) {
+  uint64_t e[K];
   if constexpr (TAU1) {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const float2 f = f2_unpack(z[k]);
-      nc[k] = f2_pack(-sigmoid_down<T>(f.x), -sigmoid_down<T>(f.y));
+      e[k] = f2_pack(exp_neg_abs<T>(f.x), exp_neg_abs<T>(f.y));
+      slope[k] = sigmoid_down(z[k], e[k]);
+      nc[k] = f2_neg(slope[k]);
+      if (SLOPE) slope[k] = f2_fma(nc[k], slope[k], slope[k]);
     }
   } else {
     uint64_t s[K];
-    softplus_neg<T>(z, s);
+    softplus_neg<T>(z, s, e);
     expm1_small<T>(s, g, nc);
     if constexpr (FAR) {
 #pragma unroll
@@ -254,43 +257,47 @@ __device__ __forceinline__ void neg_decay(const uint64_t (&z)[K], const DecayPar
         nc[k] = f2_pack(n.x, n.y);
       }
     }
+    if constexpr (SLOPE) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const uint64_t d = f2_mul(sigmoid_down(z[k], e[k]), f2_both(g.inv_tau));
+        slope[k] = f2_fma(nc[k], d, d);
+      }
+    }
   }
 }
 
-// -c of a warp's R rows of logits in shared memory, K pairs at a time. Whether some S is beyond the
-// expansion is seen from the smallest logit, before anything is computed.
+// Whether some of a warp's R rows of logits in shared memory has an S beyond the expansion: seen from
+// the smallest logit, before anything is computed.
+template <typename T, bool TAU1, int R>
+__device__ __forceinline__ bool any_far(const typename Pair<T>::Raw* zs, const DecayParams& g) {
+  using P = Pair<T>;
+  if constexpr (TAU1) return false;
+  typename P::Raw least = zs[0];
+#pragma unroll
+  for (int r = 1; r < R; ++r) least = P::least(least, zs[r * 32]);
+  const float2 f = f2_unpack(P::f32(least));
+  return fminf(f.x, f.y) < g.far_logit;
+}
+
+// -c of a warp's R rows of logits, kBatch pairs at a time.
+constexpr int kBatch = 4;
 template <typename T, bool TAU1, int R>
 __device__ __forceinline__ void row_decays(const typename Pair<T>::Raw* zs, const DecayParams& g, uint64_t (&nc)[R]) {
   using P = Pair<T>;
-  constexpr int K = 4;
   auto rows = [&](auto far) {
 #pragma unroll
-    for (int r = 0; r < R; r += K) {
-      uint64_t z[K], v[K];
+    for (int r = 0; r < R; r += kBatch) {
+      uint64_t z[kBatch], v[kBatch], unused[kBatch];
 #pragma unroll
-      for (int k = 0; k < K; ++k) z[k] = P::f32(zs[(r + k) * 32]);
-      neg_decay<T, TAU1, decltype(far)::value>(z, g, v);
+      for (int k = 0; k < kBatch; ++k) z[k] = P::f32(zs[(r + k) * 32]);
+      neg_decay<T, TAU1, decltype(far)::value, false>(z, g, v, unused);
 #pragma unroll
-      for (int k = 0; k < K; ++k) nc[r + k] = v[k];
+      for (int k = 0; k < kBatch; ++k) nc[r + k] = v[k];
     }
   };
-  bool far = false;
-  if constexpr (!TAU1) {
-    typename P::Raw least = zs[0];
-#pragma unroll
-    for (int r = 1; r < R; ++r) least = P::least(least, zs[r * 32]);
-    const float2 f = f2_unpack(P::f32(least));
-    far = fminf(f.x, f.y) < g.far_logit;
-  }
-  if (far) rows(std::true_type{});
+  if (any_far<T, TAU1, R>(zs, g)) rows(std::true_type{});
   else rows(std::false_type{});
-}
-
-// a (1 - sigmoid(z)) / tau, for padded rows (z = +inf, c = 0) zero
-template <typename T>
-__device__ __forceinline__ uint64_t decay_slope(uint64_t z, uint64_t nc, float inv_tau) {
-  const float2 f = f2_unpack(z);
-  return f2_mul(f2_mul(f2_pack(sigmoid_down<T>(f.x), sigmoid_down<T>(f.y)), f2_both(inv_tau)), f2_add(nc, f2_both(1.f)));
 }
 
 // h - c h + u
@@ -642,20 +649,31 @@ __device__ __forceinline__ void row_factors(typename Pair<T>::Raw* xs, typename 
                                             const DecayParams& gate, uint64_t (&nc)[kRowsOf<T>]) {
   using P = Pair<T>;
   constexpr int R = kRowsOf<T>;
-  row_decays<T, TAU1>(zs, gate, nc);
+  auto rows = [&](auto far) {
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const uint64_t x = P::f32(xs[r * 32]);
-    const uint64_t q = f2_mul(TIED ? f2_add(h, f2_neg(x)) : h, decay_slope<T>(P::f32(zs[r * 32]), nc[r], gate.inv_tau));
-    h = advance<TIED>(h, nc[r], x);
-    if constexpr (sizeof(T) == 4) {
-      xs[r * 32] = q;
-    } else {
-      const float2 f = f2_unpack(q);
-      xs[r * 32] = __float_as_uint(f.x);
-      zs[r * 32] = __float_as_uint(f.y);
+    for (int r0 = 0; r0 < R; r0 += kBatch) {
+      uint64_t z[kBatch], v[kBatch], slope[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) z[k] = P::f32(zs[(r0 + k) * 32]);
+      neg_decay<T, TAU1, decltype(far)::value, true>(z, gate, v, slope);
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int r = r0 + k;
+        const uint64_t x = P::f32(xs[r * 32]), q = f2_mul(TIED ? f2_add(h, f2_neg(x)) : h, slope[k]);
+        h = advance<TIED>(h, v[k], x);
+        nc[r] = v[k];
+        if constexpr (sizeof(T) == 4) {
+          xs[r * 32] = q;
+        } else {
+          const float2 f = f2_unpack(q);
+          xs[r * 32] = __float_as_uint(f.x);
+          zs[r * 32] = __float_as_uint(f.y);
+        }
+      }
     }
-  }
+  };
+  if (any_far<T, TAU1, R>(zs, gate)) rows(std::true_type{});
+  else rows(std::false_type{});
 }
 template <typename T>
 __device__ __forceinline__ uint64_t get_factor(const typename Pair<T>::Raw* xs, const typename Pair<T>::Raw* zs) {
@@ -885,8 +903,8 @@ __global__ void __launch_bounds__(128) scan_step_kernel(const StepParams p) {
     const uint64_t z = P::f32(load_pair<T, VEC>(static_cast<const T*>(p.z) + b * p.z_row + ch, n, P::inf()));
     const uint64_t x = P::f32(load_pair<T, VEC>(static_cast<const T*>(p.x) + b * p.x_row + ch, n, P::zero()));
     const uint64_t zz[1] = {z};
-    uint64_t nc[1];
-    neg_decay<T, TAU1, true>(zz, p.gate, nc);
+    uint64_t nc[1], unused[1];
+    neg_decay<T, TAU1, true, false>(zz, p.gate, nc, unused);
     const uint64_t h = advance<TIED>(load_state<VEC>(s, n), nc[0], x);
     store_state<VEC>(s, n, h);
     out = P::round(h);
