@@ -64,6 +64,7 @@ struct Pair<__nv_bfloat16> {
   static __device__ __forceinline__ uint64_t f32(Raw r) {
     return f2_pack(__uint_as_float(r << 16), __uint_as_float(r & 0xffff0000u));
   }
+  static __device__ __forceinline__ uint64_t minus(Raw r) { return f32(r ^ 0x80008000u); }
   static __device__ __forceinline__ Raw round(uint64_t v) {
     const float2 f = f2_unpack(v);
     return pack_bf162(f.x, f.y);
@@ -88,6 +89,7 @@ struct Pair<__half> {
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&r));
     return f2_pack(f.x, f.y);
   }
+  static __device__ __forceinline__ uint64_t minus(Raw r) { return f32(r ^ 0x80008000u); }
   static __device__ __forceinline__ Raw round(uint64_t v) {
     const float2 f = f2_unpack(v);
     return pack_half2(f.x, f.y);
@@ -109,6 +111,7 @@ struct Pair<float> {
   static __device__ __forceinline__ Raw zero() { return 0ull; }
   static __device__ __forceinline__ Raw inf() { return 0x7f8000007f800000ull; }
   static __device__ __forceinline__ uint64_t f32(Raw r) { return r; }
+  static __device__ __forceinline__ uint64_t minus(Raw r) { return f2_neg(r); }
   static __device__ __forceinline__ Raw round(uint64_t v) { return v; }
   static __device__ __forceinline__ Raw least(Raw a, Raw b) {
     const float2 f = f2_unpack(a), g = f2_unpack(b);
@@ -300,11 +303,11 @@ __device__ __forceinline__ void row_decays(const typename Pair<T>::Raw* zs, cons
   else rows(std::false_type{});
 }
 
-// h - c h + u
-template <bool TIED>
-__device__ __forceinline__ uint64_t advance(uint64_t h, uint64_t nc, uint64_t x) {
+// h - c h + u, x as loaded
+template <typename T, bool TIED>
+__device__ __forceinline__ uint64_t advance(uint64_t h, uint64_t nc, typename Pair<T>::Raw x) {
   h = f2_fma(nc, h, h);
-  return TIED ? f2_fma(nc, f2_neg(x), h) : f2_add(h, x);
+  return TIED ? f2_fma(nc, Pair<T>::minus(x), h) : f2_add(h, Pair<T>::f32(x));
 }
 
 // ---------------------------------------------------------------- blocks and clusters
@@ -313,7 +316,7 @@ struct alignas(16) Join {
   uint64_t p, v;
 };
 
-// Sends this block's joins to every block of the cluster and waits for theirs. What the
+// Sends this block's join to every block of the cluster, and later waits for theirs. What the
 // other warps read of the slots two steps ago is ordered before the sender's release by
 // the block barrier between, so they need not release anything themselves.
 __device__ __forceinline__ void send_join(Join* slots, int rank, int cluster, const Join& j, bool sender) {
@@ -325,7 +328,31 @@ __device__ __forceinline__ void send_join(Join* slots, int rank, int cluster, co
   } else {
     asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   }
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void receive_joins() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// Joins a block's warps in their order: what comes before warp w, and all of them.
+template <int WARPS>
+__device__ __forceinline__ void join_warps(const Join (*wj)[32], int w, Join& before, Join& all) {
+  before = all = Join{f2_both(1.f), 0ull};
+#pragma unroll
+  for (int j = 0; j < WARPS; ++j) {
+    if (j == w) before = all;
+    const Join q = wj[j][lane_id()];
+    all.v = f2_fma(q.p, all.v, q.v);
+    all.p = f2_mul(q.p, all.p);
+  }
+}
+// The cluster's blocks in their order: returns what `carry` is before block `rank`, and takes
+// `carry` past all of them.
+__device__ __forceinline__ uint64_t pass_blocks(const Join* slots, int rank, int cluster, uint64_t& carry) {
+  uint64_t mine = carry;
+  for (int j = 0; j < cluster; ++j) {
+    if (j == rank) mine = carry;
+    const Join q = slots[j * 32 + lane_id()];
+    carry = f2_fma(q.p, carry, q.v);
+  }
+  return mine;
 }
 
 // The valid rows of the chunks a warp takes one after another. The mask of a chunk decides which
@@ -446,27 +473,26 @@ __device__ __forceinline__ void put(const uint8_t* from, const Lane<T, VEC>& l, 
   }
 }
 
-// ---------------------------------------------------------------- forward
+// ---------------------------------------------------------------- forward, rows split over a cluster
+// Every step takes cluster x kWarps chunks. The next step's gates and local results are made between
+// sending a step's joins and waiting for the other blocks'.
 constexpr int kWarps = 16;
-constexpr int kForwardStages = 2;  // steps of rows in shared memory: one used, one on its way
-constexpr int kForwardRows = kWarps * kForwardStages * 2 * kRowsBytes;
 constexpr int kSlots = 2 * 32 * sizeof(Join);  // what one block of a cluster sends, double-buffered
+constexpr int kForwardRows = kWarps * 3 * 2 * kRowsBytes;  // three steps: two used, one on its way
 
 template <typename T, bool VEC, bool TAU1, bool TIED>
 __global__ void __launch_bounds__(kWarps * 32, 1) scan_forward_kernel(const ScanParams p) {
   using P = Pair<T>;
   using Raw = typename P::Raw;
-  constexpr int R = kRowsOf<T>, kRows = kWarps * R, kStages = kForwardStages;
+  constexpr int R = kRowsOf<T>, kRows = kWarps * R;
   extern __shared__ __align__(128) uint8_t dynamic[];
   __shared__ Join warps[2][kWarps][32];
   const int cluster = p.cluster, rank = cluster > 1 ? cluster_ctarank() : 0;
   const int w = warp_id(), lane = lane_id(), b = blockIdx.y;
   const int c0 = blockIdx.x / cluster * 64, ch = c0 + 2 * lane, n = min(max(p.D - ch, 0), 2);
-  uint8_t* mine = dynamic + w * kStages * 2 * kRowsBytes;
+  uint8_t* mine = dynamic + w * 3 * 2 * kRowsBytes;
   const size_t state_at = static_cast<size_t>(b) * p.D + ch;
   const int chunks = (p.L + R - 1) / R, steps = (p.L + cluster * kRows - 1) / (cluster * kRows);
-
-  uint32_t coming;  // valid rows on their way
   const bool inside = c0 + 64 <= p.D;
   Lane<T, VEC> lx(p.x, b, c0, p.D), lz(p.z, b, c0, p.D), lo(p.h, b, c0, p.D);
   const int first = (rank * kWarps + w) * R;
@@ -474,76 +500,69 @@ __global__ void __launch_bounds__(kWarps * 32, 1) scan_forward_kernel(const Scan
   ValidRows<R> valid(p, b);
   valid.look(first);
   auto start_step = [&](int step) {
+    uint32_t bits = 0;
     if (step < steps) {
-      uint8_t* to = mine + step % kStages * 2 * kRowsBytes;
-      coming = valid.take(first + step * cluster * kRows, first + (step + 1) * cluster * kRows);
-      const bool full = inside && coming == (1u << R) - 1u;
-      fetch<T, VEC>(to, lx, full, coming, P::zero());
-      fetch<T, VEC>(to + kRowsBytes, lz, full, coming, P::inf());
+      uint8_t* to = mine + step % 3 * 2 * kRowsBytes;
+      bits = valid.take(first + step * cluster * kRows, first + (step + 1) * cluster * kRows);
+      const bool full = inside && bits == (1u << R) - 1u;
+      fetch<T, VEC>(to, lx, full, bits, P::zero());
+      fetch<T, VEC>(to + kRowsBytes, lz, full, bits, P::inf());
       lx.move(cluster * kRows), lz.move(cluster * kRows);
     }
     copies_commit();
+    return bits;
   };
-
-  start_step(0);
-  uint64_t carry = p.h0 ? load_state<VEC>(p.h0 + state_at, n) : 0ull;
-  if (cluster > 1) cluster_sync();  // every block runs before another writes to it
-  for (int step = 0; step < steps; ++step) {
-    const int t0 = ((step * cluster + rank) * kWarps + w) * R;
-    const uint32_t now = coming;
-    __syncwarp();  // the lanes have read what the next copy overwrites
-    start_step(step + 1);
+  auto rows_of = [&](int step) { return reinterpret_cast<Raw*>(mine + step % 3 * 2 * kRowsBytes) + lane; };
+  auto local = [&](int step, uint64_t (&nc)[R]) {
     copies_wait<1>();
     __syncwarp();
-    uint8_t* rows = mine + step % kStages * 2 * kRowsBytes;
-    Raw* xs = reinterpret_cast<Raw*>(rows) + lane;
-    const Raw* zs = xs + kRowsBytes / sizeof(Raw);
-    uint64_t nc[R];
-    row_decays<T, TAU1>(zs, p.gate, nc);
+    const Raw* xs = rows_of(step);
+    row_decays<T, TAU1>(xs + kRowsBytes / sizeof(Raw), p.gate, nc);
     Join join{f2_both(1.f), 0ull};
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      join.v = advance<TIED>(join.v, nc[r], P::f32(xs[r * 32]));
+      join.v = advance<T, TIED>(join.v, nc[r], xs[r * 32]);
       join.p = f2_fma(nc[r], join.p, join.p);
     }
-    Join(*wj)[32] = warps[step & 1];
-    wj[w][lane] = join;
+    warps[step & 1][w][lane] = join;
+  };
+
+  uint32_t now = start_step(0), next = start_step(1);
+  uint64_t carry = p.h0 ? load_state<VEC>(p.h0 + state_at, n) : 0ull;
+  if (cluster > 1) cluster_sync();  // every block runs before another writes to it
+  uint64_t nc[R], nc_next[R];
+  local(0, nc);
+  for (int step = 0; step < steps; ++step) {
+    const int t0 = first + step * cluster * kRows;
     __syncthreads();
+    Join before, all;
+    join_warps<kWarps>(warps[step & 1], w, before, all);
+    Join* slots = reinterpret_cast<Join*>(dynamic + kForwardRows) + (step & 1) * cluster * 32;
+    if (cluster > 1) send_join(slots, rank, cluster, all, w == 0);
+    const uint32_t after = start_step(step + 2);
+    if (step + 1 < steps) local(step + 1, nc_next);
     uint64_t h = carry;
-    if (cluster == 1) {
-#pragma unroll
-      for (int j = 0; j < kWarps; ++j) {
-        if (j == w) h = carry;
-        const Join q = wj[j][lane];
-        carry = f2_fma(q.p, carry, q.v);
-      }
+    if (cluster > 1) {
+      receive_joins();
+      h = pass_blocks(slots, rank, cluster, carry);
     } else {
-      Join before{f2_both(1.f), 0ull}, all{f2_both(1.f), 0ull};
-#pragma unroll
-      for (int j = 0; j < kWarps; ++j) {
-        if (j == w) before = all;
-        const Join q = wj[j][lane];
-        all.v = f2_fma(q.p, all.v, q.v);
-        all.p = f2_mul(q.p, all.p);
-      }
-      Join* slots = reinterpret_cast<Join*>(dynamic + kForwardRows) + (step & 1) * cluster * 32;
-      send_join(slots, rank, cluster, all, w == 0);
-      for (int j = 0; j < cluster; ++j) {
-        if (j == rank) h = carry;
-        const Join q = slots[j * 32 + lane];
-        carry = f2_fma(q.p, carry, q.v);
-      }
-      h = f2_fma(before.p, h, before.v);
+      carry = f2_fma(all.p, carry, all.v);
     }
+    h = f2_fma(before.p, h, before.v);
     if (p.saved && t0 < p.L) store_state<VEC>(p.saved + (static_cast<size_t>(b) * chunks + t0 / R) * p.D + ch, n, h);
+    Raw* xs = rows_of(step);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      h = advance<TIED>(h, nc[r], P::f32(xs[r * 32]));
+      h = advance<T, TIED>(h, nc[r], xs[r * 32]);
       xs[r * 32] = P::round(h);
+      nc[r] = nc_next[r];
     }
     __syncwarp();
-    if (t0 < p.L) put<T, VEC>(rows, lo, inside && now == (1u << R) - 1u, min(p.L - t0, R), now);
+    if (t0 < p.L) put<T, VEC>(mine + step % 3 * 2 * kRowsBytes, lo, inside && now == (1u << R) - 1u, min(p.L - t0, R), now);
     lo.move(cluster * kRows);
+    __syncwarp();
+    now = next;
+    next = after;
   }
   if (rank == 0 && w == 0) store_state<VEC>(p.last + state_at, n, carry);
 }
@@ -603,7 +622,7 @@ __global__ void __launch_bounds__(kRelay * 32, 2) scan_relay_kernel(const ScanPa
     Join join{f2_both(1.f), 0ull};
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      join.v = advance<TIED>(join.v, nc[r], P::f32(xs[r * 32]));
+      join.v = advance<T, TIED>(join.v, nc[r], xs[r * 32]);
       join.p = f2_fma(nc[r], join.p, join.p);
     }
     uint64_t h;
@@ -627,7 +646,7 @@ __global__ void __launch_bounds__(kRelay * 32, 2) scan_relay_kernel(const ScanPa
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      h = advance<TIED>(h, nc[r], P::f32(xs[r * 32]));
+      h = advance<T, TIED>(h, nc[r], xs[r * 32]);
       xs[r * 32] = P::round(h);
     }
     __syncwarp();
@@ -659,8 +678,9 @@ __device__ __forceinline__ void row_factors(typename Pair<T>::Raw* xs, typename 
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
         const int r = r0 + k;
-        const uint64_t x = P::f32(xs[r * 32]), q = f2_mul(TIED ? f2_add(h, f2_neg(x)) : h, slope[k]);
-        h = advance<TIED>(h, v[k], x);
+        const typename P::Raw x = xs[r * 32];
+        const uint64_t q = f2_mul(TIED ? f2_add(h, P::minus(x)) : h, slope[k]);
+        h = advance<T, TIED>(h, v[k], x);
         nc[r] = v[k];
         if constexpr (sizeof(T) == 4) {
           xs[r * 32] = q;
@@ -777,116 +797,110 @@ __global__ void __launch_bounds__(kBackRelay * 32, 2) scan_relay_backward_kernel
   }
 }
 
-// Rows split over a cluster: rank 0 and its warp 0 take the latest chunks. A chunk hands
-// down out = P in + G.
-constexpr int kBackRows = kWarps * 2 * 3 * kRowsBytes;
+// Rows split over a cluster, as in the forward: rank 0 and its warp 0 take the latest chunks.
+constexpr int kBackWarps = 11;  // three steps of x, z and dh fill the shared memory
+constexpr int kBackRows = kBackWarps * 3 * 3 * kRowsBytes;
 
 template <typename T, bool VEC, bool TAU1, bool TIED>
-__global__ void __launch_bounds__(kWarps * 32, 1) scan_backward_kernel(const ScanParams p) {
+__global__ void __launch_bounds__(kBackWarps * 32, 1) scan_backward_kernel(const ScanParams p) {
   using P = Pair<T>;
   using Raw = typename P::Raw;
   constexpr int R = kRowsOf<T>;
   extern __shared__ __align__(128) uint8_t dynamic[];
-  __shared__ Join warps[2][kWarps][32];
+  __shared__ Join warps[2][kBackWarps][32];
   const int cluster = p.cluster, rank = cluster > 1 ? cluster_ctarank() : 0;
   const int w = warp_id(), lane = lane_id(), b = blockIdx.y;
   const int c0 = blockIdx.x / cluster * 64, ch = c0 + 2 * lane, n = min(max(p.D - ch, 0), 2);
-  uint8_t* mine = dynamic + w * 2 * 3 * kRowsBytes;
+  uint8_t* mine = dynamic + w * 3 * 3 * kRowsBytes;
   const size_t state_at = static_cast<size_t>(b) * p.D + ch;
-  const int chunks = (p.L + R - 1) / R, steps = (chunks + cluster * kWarps - 1) / (cluster * kWarps);
+  const int chunks = (p.L + R - 1) / R, each = cluster * kBackWarps, steps = (chunks + each - 1) / each;
   const float* saved = p.saved + static_cast<size_t>(b) * chunks * p.D + ch;
-
-  uint32_t coming = 0;
-  uint64_t state = 0ull;
   const bool inside = c0 + 64 <= p.D;
   Lane<T, VEC> lx(p.x, b, c0, p.D), lz(p.z, b, c0, p.D), ld(p.dh, b, c0, p.D), ox(p.dx, b, c0, p.D), oz(p.dz, b, c0, p.D);
-  const int first = (chunks - 1 - (rank * kWarps + w)) * R, back = -cluster * kWarps * R;
-  lx.move(first), lz.move(first), ld.move(first), ox.move(first), oz.move(first);
+  const int last = chunks - 1 - (rank * kBackWarps + w), back = -each * R;  // this warp's chunk of step 0
+  lx.move(last * R), lz.move(last * R), ld.move(last * R), ox.move(last * R), oz.move(last * R);
   ValidRows<R> valid(p, b);
-  valid.look(first);
+  valid.look(last * R);
+  struct Step {
+    uint32_t bits;
+    uint64_t state;
+  };
   auto start_step = [&](int step) {
-    const int c = chunks - 1 - ((step * cluster + rank) * kWarps + w);
-    coming = 0;
+    const int c = last - step * each;
+    Step s{0, 0ull};
     if (step < steps) {  // with c < 0 no row is valid and nothing is read
-      coming = valid.take(c * R, c * R + back);
-      uint8_t* to = mine + (step & 1) * 3 * kRowsBytes;
-      const bool full = inside && coming == (1u << R) - 1u;
-      fetch<T, VEC>(to, lx, full, coming, P::zero());
-      fetch<T, VEC>(to + kRowsBytes, lz, full, coming, P::inf());
-      fetch<T, VEC>(to + 2 * kRowsBytes, ld, full && p.dh.ptr, p.dh.ptr ? coming : 0u, P::zero());
+      s.bits = valid.take(c * R, c * R + back);
+      uint8_t* to = mine + step % 3 * 3 * kRowsBytes;
+      const bool full = inside && s.bits == (1u << R) - 1u;
+      fetch<T, VEC>(to, lx, full, s.bits, P::zero());
+      fetch<T, VEC>(to + kRowsBytes, lz, full, s.bits, P::inf());
+      fetch<T, VEC>(to + 2 * kRowsBytes, ld, full && p.dh.ptr, p.dh.ptr ? s.bits : 0u, P::zero());
       lx.move(back), lz.move(back), ld.move(back);
-      state = c >= 0 ? load_state<VEC>(saved + static_cast<size_t>(c) * p.D, n) : 0ull;
+      if (c >= 0) s.state = load_state<VEC>(saved + static_cast<size_t>(c) * p.D, n);
     }
     copies_commit();
+    return s;
   };
-
-  start_step(0);
-  uint64_t carry = p.dlast ? load_state<VEC>(p.dlast + state_at, n) : 0ull;
-  if (cluster > 1) cluster_sync();
-  for (int step = 0; step < steps; ++step) {
-    const int c = chunks - 1 - ((step * cluster + rank) * kWarps + w);
-    const uint32_t now = coming;
-    const uint64_t h = state;
-    __syncwarp();
-    start_step(step + 1);
+  auto rows_of = [&](int step) { return reinterpret_cast<Raw*>(mine + step % 3 * 3 * kRowsBytes) + lane; };
+  constexpr int kTensor = kRowsBytes / sizeof(Raw);
+  auto local = [&](int step, uint64_t state, uint64_t (&nc)[R]) {
     copies_wait<1>();
     __syncwarp();
-    uint8_t* rows = mine + (step & 1) * 3 * kRowsBytes;
-    Raw* xs = reinterpret_cast<Raw*>(rows) + lane;
-    Raw* zs = xs + kRowsBytes / sizeof(Raw);
-    const Raw* ds = zs + kRowsBytes / sizeof(Raw);
-    uint64_t nc[R];
-    row_factors<T, TAU1, TIED>(xs, zs, h, p.gate, nc);
+    Raw* xs = rows_of(step);
+    row_factors<T, TAU1, TIED>(xs, xs + kTensor, state, p.gate, nc);
     Join join{f2_both(1.f), 0ull};
 #pragma unroll
     for (int r = R - 1; r >= 0; --r) {
-      join.v = f2_add(join.v, P::f32(ds[r * 32]));
+      join.v = f2_add(join.v, P::f32(xs[2 * kTensor + r * 32]));
       join.v = f2_fma(nc[r], join.v, join.v);
       join.p = f2_fma(nc[r], join.p, join.p);
     }
-    Join(*wj)[32] = warps[step & 1];
-    wj[w][lane] = join;
+    warps[step & 1][w][lane] = join;
+  };
+
+  Step now = start_step(0), next = start_step(1);
+  uint64_t carry = p.dlast ? load_state<VEC>(p.dlast + state_at, n) : 0ull;
+  if (cluster > 1) cluster_sync();
+  uint64_t nc[R], nc_next[R];
+  local(0, now.state, nc);
+  for (int step = 0; step < steps; ++step) {
+    const int c = last - step * each;
     __syncthreads();
+    Join before, all;
+    join_warps<kBackWarps>(warps[step & 1], w, before, all);
+    Join* slots = reinterpret_cast<Join*>(dynamic + kBackRows) + (step & 1) * cluster * 32;
+    if (cluster > 1) send_join(slots, rank, cluster, all, w == 0);
+    const Step after = start_step(step + 2);
+    if (step + 1 < steps) local(step + 1, next.state, nc_next);
     uint64_t in = carry;
-    if (cluster == 1) {
-#pragma unroll
-      for (int j = 0; j < kWarps; ++j) {
-        if (j == w) in = carry;
-        const Join v = wj[j][lane];
-        carry = f2_fma(v.p, carry, v.v);
-      }
+    if (cluster > 1) {
+      receive_joins();
+      in = pass_blocks(slots, rank, cluster, carry);
     } else {
-      Join before{f2_both(1.f), 0ull}, all{f2_both(1.f), 0ull};
-#pragma unroll
-      for (int j = 0; j < kWarps; ++j) {
-        if (j == w) before = all;
-        const Join v = wj[j][lane];
-        all.v = f2_fma(v.p, all.v, v.v);
-        all.p = f2_mul(v.p, all.p);
-      }
-      Join* slots = reinterpret_cast<Join*>(dynamic + kBackRows) + (step & 1) * cluster * 32;
-      send_join(slots, rank, cluster, all, w == 0);
-      for (int j = 0; j < cluster; ++j) {
-        if (j == rank) in = carry;
-        const Join v = slots[j * 32 + lane];
-        carry = f2_fma(v.p, carry, v.v);
-      }
-      in = f2_fma(before.p, in, before.v);
+      carry = f2_fma(all.p, carry, all.v);
     }
+    in = f2_fma(before.p, in, before.v);
+    Raw* xs = rows_of(step);
+    Raw* zs = xs + kTensor;
 #pragma unroll
     for (int r = R - 1; r >= 0; --r) {
-      const uint64_t g = f2_add(in, P::f32(ds[r * 32])), q = get_factor<T>(xs + r * 32, zs + r * 32);
+      const uint64_t g = f2_add(in, P::f32(xs[2 * kTensor + r * 32])), q = get_factor<T>(xs + r * 32, zs + r * 32);
       in = f2_fma(nc[r], g, g);
       xs[r * 32] = P::round(input_grad<TIED>(nc[r], g));
       zs[r * 32] = P::round(f2_mul(g, q));
+      nc[r] = nc_next[r];
     }
     __syncwarp();
     if (c >= 0) {
-      const bool full = inside && now == (1u << R) - 1u;
-      put<T, VEC>(rows, ox, full, min(p.L - c * R, R), now);
-      put<T, VEC>(rows + kRowsBytes, oz, full, min(p.L - c * R, R), now);
+      const bool full = inside && now.bits == (1u << R) - 1u;
+      const uint8_t* rows = mine + step % 3 * 3 * kRowsBytes;
+      put<T, VEC>(rows, ox, full, min(p.L - c * R, R), now.bits);
+      put<T, VEC>(rows + kRowsBytes, oz, full, min(p.L - c * R, R), now.bits);
     }
     ox.move(back), oz.move(back);
+    __syncwarp();
+    now = next;
+    next = after;
   }
   if (p.dh0 && rank == 0 && w == 0) store_state<VEC>(p.dh0 + state_at, n, carry);
 }
@@ -901,11 +915,11 @@ __global__ void __launch_bounds__(128) scan_step_kernel(const StepParams p) {
   if (!p.mask || p.mask[b]) {
     float* s = p.state + static_cast<size_t>(b) * p.D + ch;
     const uint64_t z = P::f32(load_pair<T, VEC>(static_cast<const T*>(p.z) + b * p.z_row + ch, n, P::inf()));
-    const uint64_t x = P::f32(load_pair<T, VEC>(static_cast<const T*>(p.x) + b * p.x_row + ch, n, P::zero()));
+    const typename P::Raw x = load_pair<T, VEC>(static_cast<const T*>(p.x) + b * p.x_row + ch, n, P::zero());
     const uint64_t zz[1] = {z};
     uint64_t nc[1], unused[1];
     neg_decay<T, TAU1, true, false>(zz, p.gate, nc, unused);
-    const uint64_t h = advance<TIED>(load_state<VEC>(s, n), nc[0], x);
+    const uint64_t h = advance<T, TIED>(load_state<VEC>(s, n), nc[0], x);
     store_state<VEC>(s, n, h);
     out = P::round(h);
   }
@@ -938,6 +952,7 @@ bool aligned_state(const float* s) { return reinterpret_cast<uintptr_t>(s) % 8 =
 // Clusters of 1 .. kMaxCluster blocks of a split-rows kernel that run at once on the current device
 // (its blocks fill an SM, and a cluster stays inside one of the GPU's SM groups: on a B200 148,
 // 74, .. 33 of 4, .. 15 of 8), asked for once a device.
+template <int KIND>  // 0: forward, 1: backward
 const int* clusters_at_once(const void* kernel, int threads, int shared) {
   constexpr int kDevices = 64;
   static int table[kDevices][kMaxCluster + 1];
@@ -1035,7 +1050,7 @@ cudaError_t launch_scan_forward(const ScanParams& params, cudaStream_t st) {
     constexpr int kRowsAtOnce = kWarps * kRowsOf<T>, kShared = kForwardRows + kMaxCluster * kSlots;
     e = allow_shared<scan_forward_kernel<T, V, U, I>>(kShared);
     if (e != cudaSuccess) return;
-    const int* at_once = clusters_at_once(reinterpret_cast<const void*>(scan_forward_kernel<T, V, U, I>), kWarps * 32, kShared);
+    const int* at_once = clusters_at_once<0>(reinterpret_cast<const void*>(scan_forward_kernel<T, V, U, I>), kWarps * 32, kShared);
     if (one_block(tiles, p.L, kRowsAtOnce, at_once[2])) {
       p.cluster = 1;
       e = launch<scan_relay_kernel<T, V, U, I>>(p, kRelay * 32, kRelayShared, st);
@@ -1060,16 +1075,16 @@ cudaError_t launch_scan_backward(const ScanParams& params, cudaStream_t st) {
   by_kind(p.dtype, vec, p.inv_tau == 1.f, p.tied, [&](auto t, auto v, auto u, auto i) {
     using T = decltype(t);
     constexpr bool V = decltype(v)::value, U = decltype(u)::value, I = decltype(i)::value;
-    constexpr int kRowsAtOnce = kWarps * kRowsOf<T>, kShared = kBackRows + kMaxCluster * kSlots;
+    constexpr int kRowsAtOnce = kBackWarps * kRowsOf<T>, kShared = kBackRows + kMaxCluster * kSlots;
     e = allow_shared<scan_backward_kernel<T, V, U, I>>(kShared);
     if (e != cudaSuccess) return;
-    const int* at_once = clusters_at_once(reinterpret_cast<const void*>(scan_backward_kernel<T, V, U, I>), kWarps * 32, kShared);
+    const int* at_once = clusters_at_once<1>(reinterpret_cast<const void*>(scan_backward_kernel<T, V, U, I>), kBackWarps * 32, kShared);
     if (one_block(tiles, p.L, kRowsAtOnce, at_once[2])) {
       p.cluster = 1;
       e = launch<scan_relay_backward_kernel<T, V, U, I>>(p, kBackRelay * 32, kBackRelayShared, st);
     } else {
       p.cluster = pick_cluster(tiles, p.L, kRowsAtOnce, at_once);
-      e = launch<scan_backward_kernel<T, V, U, I>>(p, kWarps * 32, kShared, st);
+      e = launch<scan_backward_kernel<T, V, U, I>>(p, kBackWarps * 32, kShared, st);
     }
   });
   return e;
