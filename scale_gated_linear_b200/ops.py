@@ -44,8 +44,8 @@ def _refuse(message: str, status: int = -1):
 
 
 @functools.lru_cache(maxsize=256)
-def _scan_config(device: int, dtype, D: int, tied: bool, gate_normalizer: float):
-    return _lib.ScanConfig(device, _DTYPES[dtype], D, 1 if tied else 0, gate_normalizer)
+def _scan_config(device: int, dtype, D: int, tied, gate_normalizer):
+    return _lib.ScanConfig(device, _DTYPES[dtype], D, 1 if tied else 0, float(gate_normalizer))
 
 
 @functools.lru_cache(maxsize=256)
@@ -64,29 +64,27 @@ def _check_x(name: str, t, dims: int):
 
 
 def _check_like(name: str, t, x):
-    if not isinstance(t, torch.Tensor) or t.shape != x.shape or t.dtype != x.dtype or t.device != x.device:
+    if not isinstance(t, torch.Tensor) or t.dtype is not x.dtype or t.shape != x.shape or t.device != x.device:
         _refuse(f"{name} must have the shape {tuple(x.shape)}, the dtype {x.dtype} and the device {x.device}")
 
 
 def _check_f32(name: str, t, shape, device):
-    if (not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or tuple(t.shape) != tuple(shape) or t.device != device
+    if (not isinstance(t, torch.Tensor) or t.dtype is not torch.float32 or t.shape != shape or t.device != device
             or not t.is_contiguous()):
         _refuse(f"{name} must be a contiguous float32 tensor of shape {tuple(shape)} on {device}")
 
 
 def _check_mask(mask, shape, device):
-    """The mask as uint8, contiguous [..]."""
-    if not isinstance(mask, torch.Tensor) or tuple(mask.shape) != tuple(shape) or mask.device != device:
+    if not isinstance(mask, torch.Tensor) or mask.shape != shape or mask.device != device:
         _refuse(f"mask must have the shape {tuple(shape)} and be on {device}")
     if mask.dtype not in (torch.bool, torch.uint8) or not mask.is_contiguous():
         _refuse("mask must be a contiguous bool or uint8 tensor")
-    return mask
 
 
 def _rows3(name: str, t):
     """msgla_rows of t [B, L, C]."""
     sb, sl, sc = t.stride()
-    if sc != 1 and t.shape[2] > 1:
+    if sc != 1 and t.shape[-1] > 1:
         _refuse(f"the last dimension of {name} must be contiguous")
     return _lib.Rows(t.data_ptr(), sb, sl)
 
@@ -171,17 +169,16 @@ class ScanSaved(NamedTuple):
 def _scan_args(x, gate, mask, gate_normalizer, tied, dims):
     _check_x("x", x, dims)
     _check_like("gate", gate, x)
-    if x.shape[-1] == 0:
+    shape = x.shape
+    if shape[-1] == 0:
         _refuse("x has no channels")
     if mask is not None:
-        mask = _check_mask(mask, x.shape[:-1], x.device)
-    cfg = _scan_config(x.device.index, x.dtype, x.shape[-1], bool(tied), float(gate_normalizer))
-    return cfg, mask
+        _check_mask(mask, shape[:-1], x.device)
+    return _scan_config(x.device.index, x.dtype, shape[-1], tied, gate_normalizer), shape
 
 
 def _scan_forward(x, gate, mask, initial_state, gate_normalizer, tied, save, out, stream):
-    cfg, mask = _scan_args(x, gate, mask, gate_normalizer, tied, 3)
-    B, L, D = x.shape
+    cfg, (B, L, D) = _scan_args(x, gate, mask, gate_normalizer, tied, 3)
     if initial_state is not None:
         _check_f32("initial_state", initial_state, (B, D), x.device)
     on = _on(x.device, stream, x, gate, mask, initial_state, out)
@@ -298,9 +295,8 @@ def gated_scan_step(x, gate, state, *, mask=None, gate_normalizer: float = 16.0,
     """One token of every sequence: returns h [B, D] and updates `state` (float32 [B, D])
     in place. x, gate [B, D]; mask optional [B]: where it is zero the state stays and h is
     zero. No gradients: use gated_scan for training."""
-    cfg, mask = _scan_args(x, gate, mask, gate_normalizer, tied, 2)
-    B, D = x.shape
-    _check_f32("state", state, (B, D), x.device)
+    cfg, shape = _scan_args(x, gate, mask, gate_normalizer, tied, 2)
+    _check_f32("state", state, shape, x.device)
     if torch.is_grad_enabled() and (x.requires_grad or gate.requires_grad or state.requires_grad):
         _refuse("gated_scan_step has no gradients: call it under torch.no_grad()", -2)
     on = _on(x.device, stream, x, gate, mask, state, out)
@@ -308,7 +304,7 @@ def gated_scan_step(x, gate, state, *, mask=None, gate_normalizer: float = 16.0,
         out = on.empty_like(x)
     else:
         _check_out(out, x)
-    _lib.check(_lib.load().msgla_scan_step(cfg, B, _rows2("x", x), _rows2("gate", gate), _ptr(mask), state.data_ptr(),
+    _lib.check(_lib.load().msgla_scan_step(cfg, shape[0], _rows2("x", x), _rows2("gate", gate), _ptr(mask), state.data_ptr(),
                                            _rows2("out", out), on.handle))
     return out
 
@@ -343,7 +339,7 @@ def _norm_forward(x, groups, weight, bias, gate, mask, activation, eps, center, 
         if t is not None:
             _check_f32(name, t, (C,), x.device)
     if mask is not None:
-        mask = _check_mask(mask, x.shape[:-1], x.device)
+        _check_mask(mask, x.shape[:-1], x.device)
     cfg = _norm_config(x.device.index, x.dtype, C, groups, activation, bool(center), float(eps))
     N, S = x.shape[0], 1 if x.dim() == 2 else x.shape[1]
     on = _on(x.device, stream, x, weight, bias, gate, mask, out)
