@@ -21,8 +21,9 @@ these rules raises MSGLAError before anything is launched.
 Capturing a backward pass into a CUDA graph: autograd adds a leaf's gradient on the stream
 that was current when the leaf first joined a graph that still lives. If that is an eager
 graph of the same leaf, the capture would break inside the autograd engine, so gated_scan
-and group_norm refuse a captured call then. Drop the eager outputs first, or capture the
-explicit pairs, which keep autograd out.
+and group_norm refuse a captured call then (and one whose leaf another operation of the same
+capture has used before them, which looks the same). Drop the eager outputs first, or capture
+the explicit pairs, which keep autograd out.
 """
 from __future__ import annotations
 
@@ -228,10 +229,10 @@ def _refuse_foreign_leaves(name: str, *tensors):
 
     The node of a leaf belongs to the stream it was made on and lives as long as a graph that
     holds it. A mark left on the node outlives the handle that left it only if such a graph exists."""
-    stream = torch.cuda.current_stream().cuda_stream
     for t in tensors:
         if t is None or not t.requires_grad or t.grad_fn is not None:
             continue
+        stream = _current_handle(t.device.index)
         node = torch.autograd.graph.get_gradient_edge(t).node
         seen = node.metadata.get("msgla_stream")
         node.metadata["msgla_probe"] = True
@@ -248,10 +249,10 @@ def _refuse_foreign_leaves(name: str, *tensors):
 
 class _GatedScan(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, gate, initial_state, mask, gate_normalizer, tied, stream):
-        h, last, saved = _scan_forward(x, gate, mask, initial_state, gate_normalizer, tied, True, None, stream)
+    def forward(ctx, x, gate, initial_state, mask, gate_normalizer, tied):
+        h, last, saved = _scan_forward(x, gate, mask, initial_state, gate_normalizer, tied, True, None, None)
         ctx.set_materialize_grads(False)
-        ctx.save_for_backward(x, gate, saved.mask, saved.states)
+        ctx.save_for_backward(x, gate, mask, saved.states)
         ctx.rest = saved.config, saved.has_initial_state
         return h, last
 
@@ -264,7 +265,7 @@ class _GatedScan(torch.autograd.Function):
         if dlast is not None:
             dlast = dlast.contiguous()
         dx, dgate, dstate = gated_scan_backward(dh, dlast, ScanSaved(x, gate, mask, states, *ctx.rest))
-        return dx, dgate, dstate, None, None, None, None
+        return dx, dgate, dstate, None, None, None
 
 
 def gated_scan(x, gate, *, mask=None, initial_state=None, gate_normalizer: float = 16.0, tied: bool = False,
@@ -277,14 +278,14 @@ def gated_scan(x, gate, *, mask=None, initial_state=None, gate_normalizer: float
                     leaves the state as it is, its output is zero and its row is not read.
     initial_state   optional float32 [B, D] (default zeros); pass a call's last_state to go on.
     tied            the input enters as (1 - a_t) x_t instead of x_t.
-    out             optional tensor for h (not with gradients).
+    out, stream     optional tensor for h, optional stream (neither with gradients).
     """
     if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in (x, gate, initial_state)):
-        if out is not None:
-            _refuse("out cannot be combined with gradients")
+        if out is not None or stream is not None:
+            _refuse("out and stream cannot be combined with gradients: use torch.cuda.stream(..) around both passes")
         keep = (list(_refuse_foreign_leaves("gated_scan", x, gate, initial_state))
                 if torch.cuda.is_current_stream_capturing() else None)
-        r = _GatedScan.apply(x, gate, initial_state, mask, gate_normalizer, tied, stream)
+        r = _GatedScan.apply(x, gate, initial_state, mask, gate_normalizer, tied)
         del keep
         return r
     return _scan_forward(x, gate, mask, initial_state, gate_normalizer, tied, False, out, stream)[:2]
@@ -396,9 +397,9 @@ def group_norm_backward(dy, saved: NormSaved, *, stream=None):
 
 class _GroupNorm(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, weight, bias, gate, mask, groups, activation, eps, center, stream):
-        y, saved = _norm_forward(x, groups, weight, bias, gate, mask, activation, eps, center, True, None, stream)
-        ctx.save_for_backward(x, gate, weight, bias, saved.mask, saved.stats)
+    def forward(ctx, x, weight, bias, gate, mask, groups, activation, eps, center):
+        y, saved = _norm_forward(x, groups, weight, bias, gate, mask, activation, eps, center, True, None, None)
+        ctx.save_for_backward(x, gate, weight, bias, mask, saved.stats)
         ctx.config = saved.config
         return y
 
@@ -408,7 +409,7 @@ class _GroupNorm(torch.autograd.Function):
         if dy.stride(-1) != 1 and dy.shape[-1] > 1:
             dy = dy.contiguous()
         dx, dw, db, dgate = group_norm_backward(dy, NormSaved(*ctx.saved_tensors, ctx.config))
-        return dx, dw, db, dgate, None, None, None, None, None, None
+        return dx, dw, db, dgate, None, None, None, None, None
 
 
 def group_norm(x, groups: int, weight=None, bias=None, *, gate=None, mask=None, activation="none", eps: float = 1e-5,
@@ -424,14 +425,14 @@ def group_norm(x, groups: int, weight=None, bias=None, *, gate=None, mask=None, 
                     enter no statistic, give zeros and are not read.
     activation      "none", "silu" or "sigmoid".
     center          False: divide by the root mean square, without taking the mean off.
-    out             optional tensor for y (not with gradients).
+    out, stream     optional tensor for y, optional stream (neither with gradients).
     """
     if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in (x, weight, bias, gate)):
-        if out is not None:
-            _refuse("out cannot be combined with gradients")
+        if out is not None or stream is not None:
+            _refuse("out and stream cannot be combined with gradients: use torch.cuda.stream(..) around both passes")
         keep = (list(_refuse_foreign_leaves("group_norm", x, weight, bias, gate))
                 if torch.cuda.is_current_stream_capturing() else None)
-        r = _GroupNorm.apply(x, weight, bias, gate, mask, groups, activation, eps, center, stream)
+        r = _GroupNorm.apply(x, weight, bias, gate, mask, groups, activation, eps, center)
         del keep
         return r
     return _norm_forward(x, groups, weight, bias, gate, mask, activation, eps, center, False, out, stream)[0]

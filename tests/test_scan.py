@@ -116,10 +116,11 @@ def test_infinite_logits():
     z[:, 50] = float("-inf")
     z[:, 20:30] = float("inf")
     from scale_gated_linear_b200 import gated_scan
-    for tied in (False, True):
-        h, _ = gated_scan(x.cuda(), z.cuda(), initial_state=h0.cuda(), tied=tied)
-        parts = [gated_scan(x[:, a:b].cuda(), z[:, a:b].cuda(), tied=tied)[0] for a, b in ((10, 50), (50, 90))]
-        want = oo.scan(host(x), host(z), 16.0, tied, None, host(h0))[0]
+    for tied, tau in ((False, 16.0), (True, 16.0), (False, 1.0), (True, 1.0)):
+        kw = dict(tied=tied, gate_normalizer=tau)
+        h, _ = gated_scan(x.cuda(), z.cuda(), initial_state=h0.cuda(), **kw)
+        parts = [gated_scan(x[:, a:b].cuda(), z[:, a:b].cuda(), **kw)[0] for a, b in ((10, 50), (50, 90))]
+        want = oo.scan(host(x), host(z), tau, tied, None, host(h0))[0]
         near(h, want, 1e-5 * (1 + np.abs(want)), F32)
         for got, part in ((h[:, 10:50], parts[0]), (h[:, 50:], parts[1])):  # nothing of before is left
             near(got, host(part), 1e-5 * (1 + np.abs(host(part))), F32)
@@ -258,6 +259,36 @@ def test_prefill_in_parts_and_steps_go_on():
     near(state, wlast, 2 * e[:, -1], F32)
 
 
+def test_gradients_of_nothing_are_zero():
+    from scale_gated_linear_b200 import gated_scan_backward, gated_scan_forward
+    x, z, _, h0, _, _ = (None if t is None else t.cuda() for t in inputs(2, 70, 40, BF16, state=True, seed=19))
+    for g in gated_scan_backward(None, None, gated_scan_forward(x, z, initial_state=h0)[2]):
+        assert not g.any()
+
+
+@pytest.mark.parametrize("D,L", [(64, 5000), (1024, 2500), (4096, 600), (4160, 600)])
+def test_forms_agree(D, L):
+    """Rows split over clusters of several sizes, and one block a tile: parts of a sequence that
+    take other forms give what the whole gives, up to the f32 bound."""
+    from scale_gated_linear_b200 import gated_scan, gated_scan_backward, gated_scan_forward
+    x, z, _, _, dh, _ = (None if t is None else t.cuda() for t in inputs(1, L, D, F32, bias=2.0, seed=D))
+    h, last, saved = gated_scan_forward(x, z, tied=True)
+    dx, dz, _ = gated_scan_backward(dh, None, saved)
+    cut = 200
+    state, hs = gated_scan(x[:, :cut], z[:, :cut], tied=True)[1], []
+    tail = gated_scan(x[:, cut:], z[:, cut:], initial_state=state, tied=True)
+    for c in range(0, D, 64):  # tile by tile
+        part = slice(c, min(c + 64, D))
+        if c % 1024 == 0:
+            a, _, s = gated_scan_forward(x[..., part], z[..., part], tied=True)
+            b, g, _ = gated_scan_backward(dh[..., part], None, s)
+            hs.append((h[..., part] - a).abs().max() <= 1e-5 * a.abs().max())
+            hs.append((dx[..., part] - b).abs().max() <= 1e-5 * b.abs().max())
+            hs.append((dz[..., part] - g).abs().max() <= 1e-5 * g.abs().max())
+    assert all(hs)
+    assert (tail[0] - h[:, cut:]).abs().max() <= 1e-5 * h.abs().max() and (tail[1] - last).abs().max() <= 1e-5 * last.abs().max()
+
+
 def test_empty_calls():
     from scale_gated_linear_b200 import gated_scan, gated_scan_backward, gated_scan_forward, gated_scan_step
     e = lambda *s: torch.empty(*s, dtype=BF16, device="cuda")
@@ -378,6 +409,7 @@ def test_refusals():
         lambda: gated_scan(x, x.clone(), out=torch.zeros(1, 9, 16, dtype=BF16, device="cuda").expand(2, 9, 16)),
         lambda: gated_scan(x[..., :0], x[..., :0]),
         lambda: gated_scan(x.float().requires_grad_(), x.float(), out=x.float()),
+        lambda: gated_scan(x.float().requires_grad_(), x.float(), stream=torch.cuda.Stream()),
         lambda: gated_scan_backward(x.float(), None, gated_scan_forward(x, x)[2]),
         lambda: gated_scan_backward(x, s[:1], gated_scan_forward(x, x)[2]),
         lambda: gated_scan_step(x[:, 0], x[:, 0], s.bfloat16()), lambda: gated_scan_step(x[:, 0], x[:, 0], s.t().contiguous().t()),
