@@ -14,6 +14,9 @@
 //   shared memory and written once a block. The next row is loaded while one is computed.
 // * otherwise two passes over blocks of rows and channels: sums first, then the result, which
 //   reads x (and dy) again, from L2 where a pass fits there.
+// Measured, bf16: 65536 groups of 512 (16384 x 2048) under an output gate forward 37 us (82 % of copy
+// bandwidth), backward 73 and 6 for the weights (70 %); 8 x 2048 x 1024 in 32 groups with padding
+// 41 us forward, 57 backward.
 // Variances are sums of squared differences: from the mean itself in registers, else from each
 // thread's first value, joined by count, mean and sum of squares, so that a mean far
 // from zero costs no digits. Everything is summed in f32 in a fixed order.
@@ -324,7 +327,7 @@ __device__ __forceinline__ void copies_wait() {
 // Weight gradients: partial sums [blocks][2][C] (dw, db) in the workspace. Rows come through
 // shared memory, two ahead, each lane copying what it reads itself: held in registers, the
 // next row's 24 words beside the sums' 32 were moved behind the arithmetic or spilled (123 us
-// where this takes 80, at 65536 groups of 512).
+// where this takes 73, at 65536 groups of 512).
 constexpr int kAhead = 2;
 template <typename T, int V, int NV>
 constexpr int kRowStage = kThreads * NV * 3 * (V == 1 ? 4 : 16);  // bytes of a block's rows

@@ -11,20 +11,26 @@
 // A padded row has c = 0 and u = 0 and is not read: its logit is taken as +inf.
 //
 // Bound: HBM. Forward 3 tensors a pass (x, z in, h out), backward 5 (x, z, dh in, dx, dz
-// out); the forward states that the backward needs are rebuilt from one saved f32
-// state per 64 rows (3 % of a 16-bit tensor), which costs less than reading h would and
-// keeps them in 32 bits. The next bound is the issue rate: at the full rate of HBM the
-// SMs have 33 (forward) and 55 (backward) issue slots an element, so the gate runs on
-// packed f32x2 polynomials with one ex2 an element.
+// out); the forward states that the backward needs are rebuilt from one saved f32 state a chunk
+// of 16 rows (8 of f32; an eighth of a tensor's bytes), which costs less than reading h would
+// and keeps them in 32 bits. Next to it the issue rate: at HBM's rate the SMs have 33 (forward)
+// and 55 (backward) issue slots an element, and spend 26 and 42. So the gate runs on packed
+// f32x2 polynomials with one ex2 an element, accurate in c and not only in a: the hardware's
+// log2 alone is off by 2^-22 of one, which is all of c for a gate near one.
 //
-// Split: channels are independent, rows are a chain. A block takes 64 channels (two a
-// lane, so a warp reads whole 128-byte lines of 16-bit rows) and W x R rows at a time,
-// every warp R neighbouring rows held in registers: one pass over them gives the warp's
-// decay product and local end state, the W warps' are joined in shared memory, and a
-// second pass over the registers gives the rows from the true start. Where one block
-// per channel tile leaves SMs idle, a cluster of 2, 4 or 8 blocks shares the tile's rows
-// and passes the joined pairs through distributed shared memory, one cluster barrier a
-// step. The next step's rows are loaded before this step's are joined.
+// Split: channels are independent, rows are a chain. A block takes 64 channels (two a lane, so a
+// warp reads whole lines), a warp a chunk of rows: copied to shared memory while the chunk
+// before is computed; one pass for the chunk's decay product and local end value; then, once the
+// value before it is known, a second pass for the rows, which leave through shared memory in
+// 16-byte stores. How that value comes:
+// * one block per tile and sequence: from warp to warp, a relay. The warps are at different places
+//   of their chunks, so loads, gates and stores overlap, and one block keeps its SM busy: 90 %
+//   of copy bandwidth where the tiles are a whole number an SM (296 tiles of 8192 rows, bf16),
+//   68 % at 8 x 2048 x 2048, whose 256 tiles give 108 SMs two and 40 one;
+// * few tiles: rows split over the blocks of a cluster, joined through distributed shared memory
+//   every step (32768 x 1024: 99 us against 310 of one block a tile).
+// Before: one thread a channel 1310 us at 8 x 2048 x 2048; rows in registers with a block
+// barrier a step 75; a warp of its own for the chain, fed by the others, 52; the relay 45.
 #include <cmath>
 #include <mutex>
 #include <type_traits>
@@ -311,7 +317,7 @@ __device__ __forceinline__ uint64_t advance(uint64_t h, uint64_t nc, typename Pa
 }
 
 // ---------------------------------------------------------------- blocks and clusters
-// What W warps hand over: the decay product and local end value of their rows.
+// What a chunk hands over: the decay product and local end value of its rows.
 struct alignas(16) Join {
   uint64_t p, v;
 };
