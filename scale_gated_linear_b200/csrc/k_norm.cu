@@ -885,6 +885,260 @@ __global__ void __launch_bounds__(kThreads, 2) norm_grad_apply_kernel(const Norm
   });
 }
 
+// ---------------------------------------------------------------- samples held in shared memory
+// A cluster of blocks holds a sample's rows of one tile (whole groups of channels) in shared memory:
+// x, or x, dy and gate, are read from HBM once, and the group sums pass between the blocks through
+// distributed shared memory. A thread copies and uses the same 16-byte vectors throughout,
+// so only sums and valid rows need barriers.
+struct HoldPlan {
+  int cluster, rows;      // blocks a sample and tile, rows a block
+  int tx, ty, width;      // vectors along the tile, rows at once, channels
+  int tiles, groups;      // tiles, groups a tile
+  int shared;             // bytes
+};
+constexpr int kMaxHold = 8, kMaxHoldGroups = 32;
+
+template <typename T, int V, int TENSORS>
+struct Hold {
+  uint4* data;       // [tensor][row][tx]
+  float2* red;       // [kThreads]
+  float2* slots;     // [2][cluster][groups + 1], written by the cluster's blocks
+  uint8_t* valid;    // [rows]
+  const HoldPlan& q;
+  int rank, tx, ty, c, tile, rows;
+  long long n, s0;
+  bool here;         // the thread has a vector
+  __device__ __forceinline__ Hold(const NormParams& p, const HoldPlan& plan, uint8_t* dynamic) : q(plan) {
+    data = reinterpret_cast<uint4*>(dynamic);
+    red = reinterpret_cast<float2*>(data + static_cast<size_t>(TENSORS) * q.rows * q.tx);
+    slots = red + kThreads;
+    valid = reinterpret_cast<uint8_t*>(slots + 2 * q.cluster * (q.groups + 1));
+    rank = q.cluster > 1 ? cluster_ctarank() : 0;
+    const unsigned unit = blockIdx.x / q.cluster;
+    tile = unit % q.tiles;
+    n = unit / q.tiles;
+    tx = threadIdx.x % q.tx;
+    ty = threadIdx.x / q.tx;
+    c = tile * q.width + tx * V;
+    here = ty < q.ty && c < p.C;
+    s0 = static_cast<long long>(rank) * q.rows;
+    const long long left = p.S - s0;
+    rows = left < 0 ? 0 : left < q.rows ? static_cast<int>(left) : q.rows;
+    for (int r = threadIdx.x; r < rows; r += kThreads) valid[r] = !p.mask || p.mask[n * p.S + s0 + r];
+    __syncthreads();
+  }
+  __device__ __forceinline__ void copy(int tensor, const Rows& r) {
+    if (!here) return;
+    const T* from = at<T>(r, n, s0 + ty, c);
+    for (int row = ty; row < rows; row += q.ty, from += q.ty * r.row)
+      if (valid[row]) copy16(smem_u32(data + (tensor * q.rows + row) * q.tx + tx), from);
+  }
+  __device__ __forceinline__ void get(int tensor, int row, float (&f)[V]) const {
+    const uint4 u = data[(tensor * q.rows + row) * q.tx + tx];
+    Vec<T, V> v;
+    v.w[0] = u.x, v.w[1] = u.y, v.w[2] = u.z, v.w[3] = u.w;
+    unpack(v, f);
+  }
+  // Sums `mine` over the threads of every group and the cluster's blocks, in that order; every thread
+  // gets its group's. extra: summed over blocks alone. `turn` takes the slots' halves in turn.
+  __device__ __forceinline__ float2 group_sum(float2 mine, float extra, int turn, int cg, float& extra_sum) {
+    red[threadIdx.x] = here ? mine : make_float2(0.f, 0.f);
+    __syncthreads();
+    const int stride = q.groups + 1, wide = cg / V;
+    float2* half = slots + turn * q.cluster * stride;
+    for (int g = warp_id(); g < q.groups; g += kThreads / 32) {
+      float2 s = make_float2(0.f, 0.f);
+      for (int i = lane_id(); i < wide * q.ty; i += 32) {
+        const float2 v = red[i / wide * q.tx + g * wide + i % wide];
+        s.x += v.x;
+        s.y += v.y;
+      }
+      s.x = team_sum(s.x, 32);
+      s.y = team_sum(s.y, 32);
+      put_slot(half + rank * stride + g, s);
+    }
+    if (warp_id() == 0) put_slot(half + rank * stride + q.groups, make_float2(extra, 0.f));
+    if (q.cluster > 1) cluster_sync();
+    else __syncthreads();
+    const int g = min(tx * V / cg, q.groups - 1);
+    float2 s = make_float2(0.f, 0.f);
+    extra_sum = 0.f;
+    for (int r = 0; r < q.cluster; ++r) {
+      const float2 v = half[r * stride + g];
+      s.x += v.x;
+      s.y += v.y;
+      extra_sum += half[r * stride + q.groups].x;
+    }
+    return s;
+  }
+  // lane r writes v to block r's copy
+  __device__ __forceinline__ void put_slot(float2* slot, float2 v) {
+    const int r = lane_id();
+    if (r >= q.cluster) return;
+    if (q.cluster == 1) {
+      *slot = v;
+    } else {
+      const uint32_t to = mapa_shared(smem_u32(slot), r);
+      st_cluster_u32(to, __float_as_uint(v.x));
+      st_cluster_u32(to + 4, __float_as_uint(v.y));
+    }
+  }
+  __device__ __forceinline__ float valid_rows() const {  // of this block, in every thread of warp 0
+    int k = 0;
+    for (int r = lane_id(); r < rows; r += 32) k += valid[r];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) k += __shfl_xor_sync(~0u, k, o);
+    return static_cast<float>(k);
+  }
+};
+
+template <typename T, int V>
+__global__ void __launch_bounds__(kThreads, 3) norm_hold_forward_kernel(const NormParams p, const HoldPlan q) {
+  extern __shared__ __align__(16) uint8_t dynamic[];
+  Hold<T, V, 1> h(p, q, dynamic);
+  const int cg = p.C / p.G;
+  h.copy(0, p.x);
+  copies_commit();
+  float w[V], b[V];
+  weights<V>(p.w, h.c, h.here, 1.f, w);
+  weights<V>(p.b, h.c, h.here, 0.f, b);
+  if (q.cluster > 1) cluster_sync();  // every block runs before another writes to it
+  copies_wait<0>();
+  float sum = 0.f, count;
+  if (h.here)
+    for (int row = h.ty; row < h.rows; row += q.ty)
+      if (h.valid[row]) {
+        float f[V];
+        h.get(0, row, f);
+#pragma unroll
+        for (int e = 0; e < V; ++e) sum += f[e];
+      }
+  const float2 total = h.group_sum(make_float2(sum, 0.f), h.valid_rows(), 0, cg, count);
+  const float elements = fmaxf(count * cg, 1.f), mean = p.center ? total.x / elements : 0.f;
+  float squares = 0.f;
+  if (h.here)
+    for (int row = h.ty; row < h.rows; row += q.ty)
+      if (h.valid[row]) {
+        float f[V];
+        h.get(0, row, f);
+#pragma unroll
+        for (int e = 0; e < V; ++e) squares = fmaf(f[e] - mean, f[e] - mean, squares);
+      }
+  const float rstd = 1.f / sqrtf(h.group_sum(make_float2(squares, 0.f), 0.f, 1, cg, count).x / elements + p.eps);
+  if (!h.here) return;
+  if (p.stats && h.rank == 0 && h.ty == 0 && h.c % cg == 0)
+    *reinterpret_cast<float2*>(p.stats + 2 * (h.n * p.G + h.c / cg)) = make_float2(mean, rstd);
+#pragma unroll
+  for (int e = 0; e < V; ++e) w[e] *= rstd;
+  by_act(p.act, p.gate.ptr, [&](auto kind, auto gated) {
+    T* to = at<T>(p.y, h.n, h.s0 + h.ty, h.c);
+    const T* gp = at<T>(p.gate, h.n, h.s0 + h.ty, h.c);
+#pragma unroll 2
+    for (int row = h.ty; row < h.rows; row += q.ty, to += q.ty * p.y.row, gp += q.ty * p.gate.row) {
+      Vec<T, V> y = zeros<T, V>();
+      if (h.valid[row]) {
+        float f[V], g[V];
+        if (gated) unpack(load<T, V>(gp), g);
+        h.get(0, row, f);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const float v = fmaf(f[e] - mean, w[e], b[e]);
+          f[e] = gated ? v * act<kind>(g[e]) : act<kind>(v);
+        }
+        y = pack<T, V>(f);
+      }
+      store<T, V>(to, y);
+    }
+  });
+}
+
+// Weight gradients: partial sums of every block as chan[(n * cluster + rank)][2][C].
+template <typename T, int V, bool GATED>
+__global__ void __launch_bounds__(kThreads, 2) norm_hold_backward_kernel(const NormParams p, const HoldPlan q, float* chan) {
+  griddep_launch();
+  extern __shared__ __align__(16) uint8_t dynamic[];
+  Hold<T, V, GATED ? 3 : 2> h(p, q, dynamic);
+  const int cg = p.C / p.G;
+  h.copy(0, p.x);
+  h.copy(1, p.dy);
+  if (GATED) h.copy(2, p.gate);
+  copies_commit();
+  float w[V], b[V], dw[V] = {}, db[V] = {};
+  weights<V>(p.w, h.c, h.here, 1.f, w);
+  weights<V>(p.b, h.c, h.here, 0.f, b);
+  const float2 st = h.here ? *reinterpret_cast<const float2*>(p.stats + 2 * (h.n * p.G + h.c / cg)) : make_float2(0.f, 0.f);
+  if (q.cluster > 1) cluster_sync();
+  copies_wait<0>();
+  float2 sums = make_float2(0.f, 0.f);
+  by_act(p.act, GATED, [&](auto kind, auto) {
+    if (h.here)
+      for (int row = h.ty; row < h.rows; row += q.ty)
+        if (h.valid[row]) {
+          float x[V], dy[V], g[V], dg;
+          h.get(0, row, x);
+          h.get(1, row, dy);
+          if (GATED) h.get(2, row, g);
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            const float xh = (x[e] - st.x) * st.y;
+            const float t = grad_v<kind, GATED>(fmaf(xh, w[e], b[e]), dy[e], GATED ? g[e] : 0.f, dg);
+            dw[e] = fmaf(t, xh, dw[e]);
+            db[e] += t;
+          }
+        }
+  });
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    sums.x = fmaf(db[e], w[e], sums.x);
+    sums.y = fmaf(dw[e], w[e], sums.y);
+  }
+  float count;
+  sums = h.group_sum(sums, h.valid_rows(), 0, cg, count);
+  const float elements = fmaxf(count * cg, 1.f), m1 = p.center ? sums.x / elements : 0.f, m2 = sums.y / elements;
+  by_act(p.act, GATED, [&](auto kind, auto) {
+    if (!h.here) return;
+    T* ox = at<T>(p.dx, h.n, h.s0 + h.ty, h.c);
+    T* og = at<T>(p.dgate, h.n, h.s0 + h.ty, h.c);
+    for (int row = h.ty; row < h.rows; row += q.ty, ox += q.ty * p.dx.row, og += q.ty * p.dgate.row) {
+      Vec<T, V> dx = zeros<T, V>(), dgate = dx;
+      if (h.valid[row]) {
+        float x[V], dy[V], g[V], dg[V];
+        h.get(0, row, x);
+        h.get(1, row, dy);
+        if (GATED) h.get(2, row, g);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const float xh = (x[e] - st.x) * st.y;
+          const float t = grad_v<kind, GATED>(fmaf(xh, w[e], b[e]), dy[e], GATED ? g[e] : 0.f, dg[e]) * w[e];
+          x[e] = (t - m1 - xh * m2) * st.y;
+        }
+        dx = pack<T, V>(x);
+        if (GATED) dgate = pack<T, V>(dg);
+      }
+      store<T, V>(ox, dx);
+      if (GATED) store<T, V>(og, dgate);
+    }
+  });
+  if (!p.dw && !p.db) return;
+  // the block's sum of every channel, its rows in order, through the place of x
+  __syncthreads();
+  float2* cell = reinterpret_cast<float2*>(dynamic);
+  if (h.here)
+#pragma unroll
+    for (int e = 0; e < V; ++e) cell[h.ty * q.width + h.tx * V + e] = make_float2(dw[e], db[e]);
+  __syncthreads();
+  float* out = chan + (h.n * q.cluster + h.rank) * 2 * p.C;
+  for (int i = threadIdx.x; i < q.width && h.tile * q.width + i < p.C; i += kThreads) {
+    float2 s = cell[i];
+    for (int r = 1; r < q.ty; ++r) {
+      s.x += cell[r * q.width + i].x;
+      s.y += cell[r * q.width + i].y;
+    }
+    out[h.tile * q.width + i] = s.x;
+    out[p.C + h.tile * q.width + i] = s.y;
+  }
+}
+
 // ---------------------------------------------------------------- plans and launches
 int multiprocessors() {
   int dev = 0, n = 148;
@@ -946,6 +1200,36 @@ BlockPlan block_plan(const NormParams& p, int v, int per_sm) {
   q.rows = static_cast<int>((rows_at_once + chunks - 1) / chunks) * q.ty;
   q.chunks = static_cast<int>((p.S + q.rows - 1) / q.rows);
   return q;
+}
+
+// Whether samples can be held in shared memory, and how: tiles of whole groups from 128 bytes on,
+// and of 64 KB a block (several blocks an SM, one loading while another computes) to the 200 KB
+// that eight blocks of a cluster can hold at most; with few samples and tiles more blocks, down to
+// two rows a thread.
+bool hold_plan(const NormParams& p, int v, int tensors, HoldPlan& q) {
+  const int cg = p.C / p.G, least = 8 * v;
+  if (v == 1 || p.S < 2 || cg > kThreads * v) return false;
+  q.width = (least + cg - 1) / cg * cg;
+  if (q.width > p.C) q.width = p.C;
+  q.groups = q.width / cg;
+  q.tx = q.width / v;
+  q.ty = kThreads / q.tx;
+  if (q.groups > kMaxHoldGroups || q.ty < 1) return false;
+  if (q.ty > p.S) q.ty = static_cast<int>(p.S);
+  q.tiles = (p.C + q.width - 1) / q.width;
+  const long long bytes = p.S * q.tx * 16 * tensors, units = p.N * q.tiles;
+  long long c = (bytes + 65535) / 65536;
+  if (c > kMaxHold) c = kMaxHold;
+  while (c < kMaxHold && units * c < 2LL * multiprocessors() && p.S / (c + 1) >= 2 * q.ty) ++c;
+  const long long rows = (p.S + c - 1) / c;
+  if (rows * q.tx * 16 * tensors > 200 * 1024 || units * c > 0x7fffffffLL) return false;
+  q.rows = static_cast<int>(rows);
+  q.cluster = static_cast<int>(c);
+  long long data = rows * q.tx * 16 * tensors;
+  const long long cells = static_cast<long long>(q.ty) * q.width * 8;
+  if (tensors > 1 && data < cells) return false;  // the weights' sums take the place of x in the end
+  q.shared = static_cast<int>(data + kThreads * 8 + 2 * c * (q.groups + 1) * 8 + rows);
+  return true;
 }
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
@@ -1014,6 +1298,24 @@ cudaError_t launch_after(void (*kernel)(KArgs...), dim3 grid, dim3 block, int sh
   return cudaLaunchKernelEx(&cfg, kernel, KArgs(args)...);
 }
 
+template <auto kernel, typename... Args>
+cudaError_t launch_hold(const HoldPlan& q, const NormParams& p, cudaStream_t st, const Args&... args) {
+  cudaError_t e = allow_shared<kernel>(212 * 1024);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.N * q.tiles * q.cluster));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = q.shared;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = q.cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 cudaError_t launch_weights(const NormParams& p, const float* part, int rows, cudaStream_t st) {
   cudaError_t e = cudaSuccess;
   if (p.dw || p.db) e = launch_after(norm_weights_kernel, dim3((p.C + 31) / 32), dim3(32, 32), 0, st, p, part, rows);
@@ -1032,6 +1334,12 @@ size_t norm_workspace(const NormParams& p, bool backward) {
       n = backward ? static_cast<size_t>(row_plan(p, v, kRowBlocksBackward).blocks) * 2 * p.C * 4 : 0;
     } else {
       n = BlockSpace(p, block_plan(p, v, backward ? kBlocksBackward : kBlocks), backward).bytes;
+      HoldPlan q;
+      for (int tensors : {2, 3})
+        if (backward && hold_plan(p, v, tensors, q)) {
+          const size_t m = static_cast<size_t>(p.N) * q.cluster * 2 * p.C * 4;
+          n = m > n ? m : n;
+        }
     }
     most = n > most ? n : most;
   }
@@ -1049,6 +1357,8 @@ cudaError_t launch_norm_forward(const NormParams& p, cudaStream_t st) {
       by_vectors<V>(p, q, [&](auto nv, auto team) {
         norm_rows_forward_kernel<T, V, decltype(nv)::value, decltype(team)::value><<<dim3(q.slices, q.blocks), kThreads, 0, st>>>(p, q);
       });
+    } else if (HoldPlan hold; hold_plan(p, v, 1, hold)) {
+      if constexpr (V > 1) e = launch_hold<norm_hold_forward_kernel<T, V>>(hold, p, st, p, hold);
     } else {
       const BlockPlan q = block_plan(p, v, kBlocks);
       const BlockSpace s(p, q, false);
@@ -1083,6 +1393,13 @@ cudaError_t launch_norm_backward(const NormParams& p, cudaStream_t st) {
         if (e == cudaSuccess) kernel<<<dim3(q.slices, q.blocks), kThreads, kRows > sums ? kRows : sums, st>>>(p, q);
       });
       if (e == cudaSuccess) e = launch_weights(p, static_cast<const float*>(p.workspace), q.blocks, st);
+    } else if (HoldPlan hold; hold_plan(p, v, p.gate.ptr ? 3 : 2, hold)) {
+      if constexpr (V > 1) {
+        float* chan = static_cast<float*>(p.workspace);
+        e = p.gate.ptr ? launch_hold<norm_hold_backward_kernel<T, V, true>>(hold, p, st, p, hold, chan)
+                       : launch_hold<norm_hold_backward_kernel<T, V, false>>(hold, p, st, p, hold, chan);
+        if (e == cudaSuccess) e = launch_weights(p, chan, static_cast<int>(p.N * hold.cluster), st);
+      }
     } else {
       const BlockPlan q = block_plan(p, v, kBlocksBackward);
       const BlockSpace s(p, q, true);
