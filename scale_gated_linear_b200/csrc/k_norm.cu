@@ -7,16 +7,19 @@
 //     dx = (dv w - <dv w> - xhat <dv w xhat>) / sqrt(var + eps)   (no centring: no <dv w>).
 // Padded rows enter no sum, give zeros and are not read.
 //
-// Bound: HBM. Two forms, by the shape alone:
+// Bound: HBM. Three forms, by shape and alignment:
 // * S = 1 and groups of up to 8192 channels: a team of 1 to 32 lanes, or a block, holds one row's
 //   group in registers, up to 32 values a lane, so every tensor moves once. Teams keep their channels from row to
 //   row: weights stay in registers, and the weight gradients are summed there, joined in
 //   shared memory and written once a block. The next row is loaded while one is computed.
-// * otherwise two passes over blocks of rows and channels: sums first, then the result, which
+// * otherwise, where a sample's rows of a tile of channels fit the shared memory of a cluster of up
+//   to eight blocks (1.6 MB in all, and rows aligned to 16 bytes), they are held there: every tensor moves
+//   once here too;
+// * else two passes over blocks of rows and channels: sums first, then the result, which
 //   reads x (and dy) again, from L2 where a pass fits there.
 // Measured, bf16: 65536 groups of 512 (16384 x 2048) under an output gate forward 37 us (82 % of copy
 // bandwidth), backward 73 and 6 for the weights (70 %); 8 x 2048 x 1024 in 32 groups with padding
-// 41 us forward, 57 backward.
+// 78 us forward and backward held in shared memory, 97 in two passes.
 // Variances are sums of squared differences: from the mean itself in registers, else from each
 // thread's first value, joined by count, mean and sum of squares, so that a mean far
 // from zero costs no digits. Everything is summed in f32 in a fixed order.
@@ -993,7 +996,7 @@ struct Hold {
 };
 
 template <typename T, int V>
-__global__ void __launch_bounds__(kThreads, 3) norm_hold_forward_kernel(const NormParams p, const HoldPlan q) {
+__global__ void __launch_bounds__(kThreads, 4) norm_hold_forward_kernel(const NormParams p, const HoldPlan q) {
   extern __shared__ __align__(16) uint8_t dynamic[];
   Hold<T, V, 1> h(p, q, dynamic);
   const int cg = p.C / p.G;
@@ -1054,7 +1057,7 @@ __global__ void __launch_bounds__(kThreads, 3) norm_hold_forward_kernel(const No
 
 // Weight gradients: partial sums of every block as chan[(n * cluster + rank)][2][C].
 template <typename T, int V, bool GATED>
-__global__ void __launch_bounds__(kThreads, 2) norm_hold_backward_kernel(const NormParams p, const HoldPlan q, float* chan) {
+__global__ void __launch_bounds__(kThreads, GATED ? 2 : 3) norm_hold_backward_kernel(const NormParams p, const HoldPlan q, float* chan) {
   griddep_launch();
   extern __shared__ __align__(16) uint8_t dynamic[];
   Hold<T, V, GATED ? 3 : 2> h(p, q, dynamic);
@@ -1203,8 +1206,9 @@ BlockPlan block_plan(const NormParams& p, int v, int per_sm) {
 }
 
 // Whether samples can be held in shared memory, and how: tiles of whole groups from 128 bytes on,
-// and of 64 KB a block (several blocks an SM, one loading while another computes) to the 200 KB
-// that eight blocks of a cluster can hold at most; with few samples and tiles more blocks, down to
+// and of 48 KB a block (three or four blocks an SM, one loading while another computes: 78 us for the
+// training pass of 8 x 2048 x 1024 with padding, 88 with two of 64 KB) to the 200 KB that each
+// of a cluster's eight blocks can hold at most; with few samples and tiles more blocks, down to
 // two rows a thread.
 bool hold_plan(const NormParams& p, int v, int tensors, HoldPlan& q) {
   const int cg = p.C / p.G, least = 8 * v;
@@ -1218,7 +1222,7 @@ bool hold_plan(const NormParams& p, int v, int tensors, HoldPlan& q) {
   if (q.ty > p.S) q.ty = static_cast<int>(p.S);
   q.tiles = (p.C + q.width - 1) / q.width;
   const long long bytes = p.S * q.tx * 16 * tensors, units = p.N * q.tiles;
-  long long c = (bytes + 65535) / 65536;
+  long long c = (bytes + 48 * 1024 - 1) / (48 * 1024);
   if (c > kMaxHold) c = kMaxHold;
   while (c < kMaxHold && units * c < 2LL * multiprocessors() && p.S / (c + 1) >= 2 * q.ty) ++c;
   const long long rows = (p.S + c - 1) / c;
