@@ -396,6 +396,9 @@ constexpr int kRowsOf = kRowsBytes / (64 * sizeof(T));
 __device__ __forceinline__ void copy16(uint32_t to, const void* from) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
+__device__ __forceinline__ void copy4(uint32_t to, const void* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
+}
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copies_wait() {
@@ -418,11 +421,16 @@ struct Lane {
     at = static_cast<T*>(r.ptr) + b * r.batch + first * r.row + c0 + c;
   }
   __device__ __forceinline__ void move(long long rows) { at += rows * row; }
+  // Without VEC: whether the lane's pair is one aligned word of 4 bytes (two of f32) in every row.
+  __device__ __forceinline__ bool words() const {
+    return sizeof(T) == 4 || (reinterpret_cast<uintptr_t>(at) % 4 == 0 && row % 2 == 0);
+  }
 };
 
 // Starts a warp's copy of R rows to `to`; rows whose bit is not set and channels past D
-// become `none`. full: every row is valid and every channel inside D. Without VEC the lanes load
-// and store their pairs at once.
+// become `none`. full: every row is valid and every channel inside D. Without VEC the lanes copy
+// their pairs word by word where they can, and load and store them at once where not (an
+// odd number of 16-bit channels).
 template <typename T, bool VEC>
 __device__ __forceinline__ void fetch(uint8_t* to, const Lane<T, VEC>& l, bool full, uint32_t bits,
                                       typename Pair<T>::Raw none) {
@@ -443,10 +451,28 @@ __device__ __forceinline__ void fetch(uint8_t* to, const Lane<T, VEC>& l, bool f
       }
     }
   } else {
+using Raw = typename Pair<T>::Raw;
+    Raw* at = reinterpret_cast<Raw*>(to) + lane;
+    constexpr int kStep = Lane<T, VEC>::kRow / sizeof(Raw);
+    if (sizeof(T) == 4) {
 #pragma unroll 4
-    for (int i = 0; i < R; ++i, from += l.row)
-      reinterpret_cast<typename Pair<T>::Raw*>(to + i * Lane<T, VEC>::kRow)[lane] =
-          load_pair<T, false>(from, bits >> i & 1 ? l.n : 0, none);
+      for (int i = 0; i < R; ++i, from += l.row, at += kStep) {
+        const int n = bits >> i & 1 ? l.n : 0;
+        if (n < 2) *at = none;
+        if (n > 0) copy4(smem_u32(at), from);
+        if (n > 1) copy4(smem_u32(at) + 4, from + 1);
+      }
+    } else if (l.words()) {
+#pragma unroll 4
+      for (int i = 0; i < R; ++i, from += l.row, at += kStep) {
+        const int n = bits >> i & 1 ? l.n : 0;
+        if (n == 2) copy4(smem_u32(at), from);
+        else *at = load_pair<T, false>(from, n, none);
+      }
+    } else {
+#pragma unroll 8
+      for (int i = 0; i < R; ++i, from += l.row) at[i * kStep] = load_pair<T, false>(from, bits >> i & 1 ? l.n : 0, none);
+    }
   }
 }
 
@@ -471,11 +497,15 @@ __device__ __forceinline__ void put(const uint8_t* from, const Lane<T, VEC>& l, 
     }
   } else {
     using Raw = typename Pair<T>::Raw;
+    const Raw* v = reinterpret_cast<const Raw*>(from) + lane;
+    const bool word = sizeof(T) == 2 && l.words() && l.n == 2;
 #pragma unroll 4
-    for (int i = 0; i < R; ++i, to += l.row)
-      if (i < rows)
-        store_pair<T, false>(to, l.n, bits >> i & 1 ? reinterpret_cast<const Raw*>(from + i * Lane<T, VEC>::kRow)[lane]
-                                                    : Pair<T>::zero());
+    for (int i = 0; i < R; ++i, to += l.row, v += Lane<T, VEC>::kRow / sizeof(Raw))
+      if (i < rows) {
+        const Raw r = bits >> i & 1 ? *v : Pair<T>::zero();
+        if (word) *reinterpret_cast<Raw*>(to) = r;
+        else store_pair<T, false>(to, l.n, r);
+      }
   }
 }
 
