@@ -28,7 +28,7 @@
 //   of copy bandwidth where the tiles are a whole number an SM (296 tiles of 8192 rows, bf16),
 //   68 % at 8 x 2048 x 2048, whose 256 tiles give 108 SMs two and 40 one;
 // * few tiles: rows split over the blocks of a cluster, joined through distributed shared memory
-//   every step (32768 x 1024: 99 us against 310 of one block a tile).
+//   every step (32 tiles of 16384 rows: 70 us against 158 of one block a tile).
 // Before: one thread a channel 1310 us at 8 x 2048 x 2048; rows in registers with a block
 // barrier a step 75; a warp of its own for the chain, fed by the others, 52; the relay 45.
 #include <cmath>
@@ -1018,7 +1018,7 @@ const int* clusters_at_once(const void* kernel, int threads, int shared) {
 // Whether one block per channel tile and sequence is the form to take, or its rows are split over a
 // cluster. A block of the first form keeps its SM busy by itself (9.5 ns a row of 64
 // channels), one of the second at half that rate or more: where two blocks a tile find an
-// SM each they win (8 tiles of 16384 rows: 39 us against 156, 64 tiles with gradients 395
+// SM each they win (8 tiles of 16384 rows: 37 us against 156, 64 tiles with gradients 333
 // against 519), unless the rows are few (256 rows: 5.8 us against 5.3, 1024: 7.4 against 12.7).
 bool one_block(long long tiles, int L, int rows, int pairs) { return tiles > pairs || L <= 2 * rows; }
 
