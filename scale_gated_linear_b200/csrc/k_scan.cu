@@ -458,7 +458,8 @@ using Raw = typename Pair<T>::Raw;
 #pragma unroll 4
       for (int i = 0; i < R; ++i, from += l.row, at += kStep) {
         const int n = bits >> i & 1 ? l.n : 0;
-        if (n < 2) *at = none;
+        if (n == 0) *at = none;
+        if (n == 1) reinterpret_cast<uint32_t*>(at)[1] = static_cast<uint32_t>(none);
         if (n > 0) copy4(smem_u32(at), from);
         if (n > 1) copy4(smem_u32(at) + 4, from + 1);
       }
