@@ -1042,7 +1042,10 @@ DecayParams decay_params(float inv_tau, int dtype) {
   DecayParams g;
   g.inv_tau = inv_tau;
   g.far = 0.5f / inv_tau;
-  g.far_logit = static_cast<float>(-std::log(std::expm1(0.5 / inv_tau)));  // softplus(-z) = far; -inf for large tau
+  // softplus(-z) = far at z = -log(e^far - 1), written without e^far: that overflows from tau = 1420 on, and
+  // with a threshold of -inf no logit at all would be taken out of the expansion's range
+  const double far = 0.5 / inv_tau;
+  g.far_logit = static_cast<float>(-(far + std::log(-std::expm1(-far))));
   double power = inv_tau;
   for (int i = 0; i < 6; ++i, power *= inv_tau) {
     const float v = static_cast<float>((dtype == kF32 ? k5 : k4)[i] * power);
