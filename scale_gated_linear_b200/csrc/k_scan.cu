@@ -230,16 +230,22 @@ __device__ __forceinline__ void expm1_small(const uint64_t (&s)[K], const DecayP
 #pragma unroll
   for (int k = 0; k < K; ++k) r[k] = f2_mul(s[k], r[k]);
 }
-// 1 - sigmoid(z), given e = e^{-|z|}
-__device__ __forceinline__ uint64_t sigmoid_down(uint64_t z, uint64_t e) {
+// 1 - sigmoid(z), given e = e^{-|z|} and r = 1 / (1 + e)
+__device__ __forceinline__ uint64_t sigmoid_down(uint64_t z, uint64_t e, uint64_t r) {
   const float2 f = f2_unpack(z), g = f2_unpack(e);
-  return f2_pack((f.x >= 0.f ? g.x : 1.f) * rcp_approx(1.f + g.x), (f.y >= 0.f ? g.y : 1.f) * rcp_approx(1.f + g.y));
+  return f2_mul(f2_pack(f.x >= 0.f ? g.x : 1.f, f.y >= 0.f ? g.y : 1.f), r);
+}
+__device__ __forceinline__ uint64_t rcp_one_plus(uint64_t e) {
+  const float2 f = f2_unpack(e);
+  return f2_pack(rcp_approx(1.f + f.x), rcp_approx(1.f + f.y));
 }
 
 // -c of K pairs of logits. With S = softplus(-z), -c = e^{-S / tau} - 1 is S times a polynomial in S
 // while S <= tau / 2; beyond (FAR: look for it), where e^{-S / tau} < 0.61 loses nothing in the
 // difference from one, it is that difference. TAU1: c = 1 - sigmoid(z) in closed form.
-// SLOPE: also -dc/dz = a (1 - sigmoid(z)) / tau; for padded rows (z = +inf) both are zero.
+// SLOPE: also -dc/dz = a (1 - sigmoid(z)) / tau, accurate relative to itself: for gates that forget a is
+// not taken as 1 - c, which has lost it, but as the exponential that c came from, and with tau = 1 the
+// slope is sigmoid(z) (1 - sigmoid(z)) = e / (1 + e)^2. For padded rows (z = +inf) both are zero.
 template <typename T, bool TAU1, bool FAR, bool SLOPE, int K>
 __device__ __forceinline__ void neg_decay(const uint64_t (&z)[K], const DecayParams& g, uint64_t (&nc)[K], uint64_t (&slope)[K]) {
   uint64_t e[K];
@@ -248,29 +254,34 @@ __device__ __forceinline__ void neg_decay(const uint64_t (&z)[K], const DecayPar
     for (int k = 0; k < K; ++k) {
       const float2 f = f2_unpack(z[k]);
       e[k] = f2_pack(exp_neg_abs<T>(f.x), exp_neg_abs<T>(f.y));
-      slope[k] = sigmoid_down(z[k], e[k]);
-      nc[k] = f2_neg(slope[k]);
-      if (SLOPE) slope[k] = f2_fma(nc[k], slope[k], slope[k]);
+      const uint64_t r = rcp_one_plus(e[k]);
+      nc[k] = f2_neg(sigmoid_down(z[k], e[k], r));
+      if (SLOPE) slope[k] = f2_mul(f2_mul(e[k], r), r);
     }
   } else {
     uint64_t s[K];
     softplus_neg<T>(z, s, e);
     expm1_small<T>(s, g, nc);
-    if constexpr (FAR) {
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const float2 f = f2_unpack(s[k]);
-        float2 n = f2_unpack(nc[k]);
-        if (f.x > g.far) n.x = ex2_approx(-kLog2e * g.inv_tau * f.x) - 1.f;
-        if (f.y > g.far) n.y = ex2_approx(-kLog2e * g.inv_tau * f.y) - 1.f;
-        nc[k] = f2_pack(n.x, n.y);
-      }
-    }
-    if constexpr (SLOPE) {
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const uint64_t d = f2_mul(sigmoid_down(z[k], e[k]), f2_both(g.inv_tau));
+    for (int k = 0; k < K; ++k) {
+      uint64_t d = 0;
+      if constexpr (SLOPE) {
+        d = f2_mul(sigmoid_down(z[k], e[k], rcp_one_plus(e[k])), f2_both(g.inv_tau));
         slope[k] = f2_fma(nc[k], d, d);
+      }
+      if constexpr (FAR) {
+        const float2 f = f2_unpack(s[k]), down = f2_unpack(d);
+        float2 n = f2_unpack(nc[k]), v = SLOPE ? f2_unpack(slope[k]) : down;
+        if (f.x > g.far) {
+          const float a = ex2_approx(-kLog2e * g.inv_tau * f.x);
+          n.x = a - 1.f, v.x = a * down.x;
+        }
+        if (f.y > g.far) {
+          const float a = ex2_approx(-kLog2e * g.inv_tau * f.y);
+          n.y = a - 1.f, v.y = a * down.y;
+        }
+        nc[k] = f2_pack(n.x, n.y);
+        if (SLOPE) slope[k] = f2_pack(v.x, v.y);
       }
     }
   }
