@@ -308,7 +308,10 @@ typedef struct msgla_rows {
  * element-wise gate and no key: the notes' S_t with Diag(alpha_t) alone), for a batch
  * of B sequences of L rows of D channels, with gate logits z in the layer's form:
  *     log a_t = logsigmoid(z_t) / gate_normalizer
- *     h_t = a_t h_{t-1} + u_t,   u_t = x_t,  or (1 - a_t) x_t when tied = 1. */
+ *     h_t = a_t h_{t-1} + u_t,   u_t = x_t,  or (1 - a_t) x_t when tied = 1.
+ * Infinities and NaN go by that formula: an infinite state stays what it is over gates above zero
+ * and padded rows, and is NaN after a gate of zero (z = -inf) or an infinity of the other sign. A
+ * sequence with such a value costs about 0.3 us a row more for its 64 neighbouring channels. */
 typedef struct msgla_scan_config {
   int device;             /* CUDA device of every buffer                               */
   int dtype;              /* msgla_dtype of x, z, h and of their gradients              */

@@ -9,6 +9,8 @@
 //     g_t = dh_t + a_{t+1} g_{t+1},  dx_t = g_t or c_t g_t,
 //     dz_t = g_t (h_{t-1} - [tied] x_t) a_t (1 - sigmoid(z_t)) / tau,  dh_0 = a_1 g_1.
 // A padded row has c = 0 and u = 0 and is not read: its logit is taken as +inf.
+// An infinite h makes NaN of h - c h where a h stays infinite: channels that end so are computed
+// again by the formula as it stands (see "values that are not finite").
 //
 // Bound: HBM. Forward 3 tensors a pass (x, z in, h out), backward 5 (x, z, dh in, dx, dz
 // out); the forward states that the backward needs are rebuilt from one saved f32 state a chunk
@@ -57,6 +59,11 @@ __device__ __forceinline__ float rcp_approx(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+
+// A warp's R rows of 64 channels take 2 KB for every type (16 rows of 128 bytes, 8 of 256).
+constexpr int kRowsBytes = 2048;
+template <typename T>
+constexpr int kRowsOf = kRowsBytes / (64 * sizeof(T));
 
 // ---------------------------------------------------------------- pairs of elements
 // Two neighbouring channels of one row, as loaded.
@@ -327,6 +334,67 @@ __device__ __forceinline__ uint64_t advance(uint64_t h, uint64_t nc, typename Pa
   return TIED ? f2_fma(nc, Pair<T>::minus(x), h) : f2_add(h, Pair<T>::f32(x));
 }
 
+// ---------------------------------------------------------------- values that are not finite
+// h - c h is NaN for an infinite h, a h is infinite. Looking at every state would cost the sequence
+// kernels issue slots in every row. But from an infinity or NaN on, a channel's values are infinite or
+// NaN to the end (a padded row keeps them, a gate of zero makes them NaN) in the fast form as in the
+// formula, so its last value tells: where that is not finite one warp computes the channel again, row by
+// row with a h itself, when everything else of the tile has been stored. The other channels keep their bits.
+// Such a tile takes about 0.3 us a row, its gradients 0.4 (8 x 2048 x 2048 bf16 with an infinity in every
+// tile: 0.61 and 0.86 ms); tiles without one take what they took before this was looked at.
+__device__ __forceinline__ uint32_t not_finite(uint64_t v, int n) {  // bit i: the i-th of n channels
+  const float2 f = f2_unpack(v);
+  return (n > 0 && !(fabsf(f.x) < INFINITY) ? 1u : 0u) | (n > 1 && !(fabsf(f.y) < INFINITY) ? 2u : 0u);
+}
+__device__ __forceinline__ void store_some(float* p, uint32_t which, uint64_t v) {
+  const float2 f = f2_unpack(v);
+  if (which & 1u) p[0] = f.x;
+  if (which & 2u) p[1] = f.y;
+}
+template <typename T>
+__device__ __forceinline__ void store_some(T* p, uint32_t which, typename Pair<T>::Raw v) {
+  if (which & 1u) p[0] = Pair<T>::half(v, 0);
+  if (which & 2u) p[1] = Pair<T>::half(v, 1);
+}
+// a h for any h, given -c and whether a is zero (a logit of -inf; bit i: the i-th channel)
+__device__ __forceinline__ uint32_t gate_zero(uint64_t z) {
+  const float2 f = f2_unpack(z);
+  return (f.x == -INFINITY ? 1u : 0u) | (f.y == -INFINITY ? 2u : 0u);
+}
+__device__ __forceinline__ float decayed(float h, float nc, bool zero) {
+  if (fabsf(h) < INFINITY) return fmaf(nc, h, h);
+  return zero ? NAN : h;
+}
+__device__ __forceinline__ uint64_t decayed(uint64_t h, uint64_t nc, uint32_t zero) {
+  const float2 f = f2_unpack(h), c = f2_unpack(nc);
+  return f2_pack(decayed(f.x, c.x, (zero & 1u) != 0), decayed(f.y, c.y, (zero & 2u) != 0));
+}
+template <typename T, bool TIED>
+__device__ __forceinline__ uint64_t advance_any(uint64_t h, uint64_t nc, uint32_t zero, typename Pair<T>::Raw x) {
+  h = decayed(h, nc, zero);
+  return TIED ? f2_fma(nc, Pair<T>::minus(x), h) : f2_add(h, Pair<T>::f32(x));
+}
+// A row's factor of its gate's gradient, kept in the places of x and z.
+template <typename T>
+__device__ __forceinline__ void set_factor(typename Pair<T>::Raw* xs, typename Pair<T>::Raw* zs, uint64_t q) {
+  if constexpr (sizeof(T) == 4) {
+    *xs = q;
+  } else {
+    const float2 f = f2_unpack(q);
+    *xs = __float_as_uint(f.x);
+    *zs = __float_as_uint(f.y);
+  }
+}
+template <typename T>
+__device__ __forceinline__ uint64_t get_factor(const typename Pair<T>::Raw* xs, const typename Pair<T>::Raw* zs) {
+  if constexpr (sizeof(T) == 4) return *xs;
+  else return f2_pack(__uint_as_float(*xs), __uint_as_float(*zs));
+}
+template <bool TIED>
+__device__ __forceinline__ uint64_t input_grad(uint64_t nc, uint64_t g) {
+  return TIED ? f2_neg(f2_mul(nc, g)) : g;
+}
+
 // ---------------------------------------------------------------- blocks and clusters
 // What a chunk hands over: the decay product and local end value of its rows.
 struct alignas(16) Join {
@@ -399,10 +467,6 @@ struct ValidRows {
 };
 
 // ---------------------------------------------------------------- rows in shared memory
-// A warp's R rows of 64 channels take 2 KB for every type (16 rows of 128 bytes, 8 of 256).
-constexpr int kRowsBytes = 2048;
-template <typename T>
-constexpr int kRowsOf = kRowsBytes / (64 * sizeof(T));
 
 __device__ __forceinline__ void copy16(uint32_t to, const void* from) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
@@ -521,6 +585,109 @@ __device__ __forceinline__ void put(const uint8_t* from, const Lane<T, VEC>& l, 
   }
 }
 
+// A warp's channels `bad` (a lane's bits 0 and 1: of its pair) of sequence b once more, from the first
+// row (see "values that are not finite"). space: shared memory that no one else uses, a chunk of x and z.
+// Both functions are compiled into every sequence kernel, so they are kept short: one chunk at a time, the
+// general form of the gate for tau = 1 too.
+template <typename T, bool TIED>
+__device__ __noinline__ void forward_again(const ScanParams& p, int b, int c0, uint32_t bad, uint8_t* space) {
+  using P = Pair<T>;
+  using Raw = typename P::Raw;
+  constexpr int R = kRowsOf<T>;
+  const int ch = c0 + 2 * lane_id(), n = min(max(p.D - ch, 0), 2), chunks = (p.L + R - 1) / R;
+  const size_t state_at = static_cast<size_t>(b) * p.D + ch;
+  const Raw* xs = reinterpret_cast<const Raw*>(space) + lane_id();
+  T* out = static_cast<T*>(p.h.ptr) + b * p.h.batch + ch;
+  Lane<T, false> lx(p.x, b, c0, p.D), lz(p.z, b, c0, p.D);
+  ValidRows<R> valid(p, b);
+  valid.look(0);
+  uint64_t h = p.h0 ? load_state<false>(p.h0 + state_at, n) : 0ull;
+#pragma unroll 1
+  for (int c = 0; c < chunks; ++c) {
+    const uint32_t bits = valid.take(c * R, (c + 1) * R);
+    fetch<T, false>(space, lx, false, bits, P::zero());
+    fetch<T, false>(space + kRowsBytes, lz, false, bits, P::inf());
+    copies_commit();
+    lx.move(R), lz.move(R);
+    if (p.saved) store_some(p.saved + (static_cast<size_t>(b) * chunks + c) * p.D + ch, bad, h);
+    copies_wait<0>();
+    const int rows = min(p.L - c * R, R);
+#pragma unroll 1
+    for (int r0 = 0; r0 < rows; r0 += kBatch) {
+      uint64_t z[kBatch], nc[kBatch], unused[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) z[k] = P::f32(xs[kRowsBytes / sizeof(Raw) + (r0 + k) * 32]);
+      neg_decay<T, false, true, false>(z, p.gate, nc, unused);
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        h = advance_any<T, TIED>(h, nc[k], gate_zero(z[k]), xs[(r0 + k) * 32]);
+        if (r0 + k < rows) store_some<T>(out + k * p.h.row, bad, bits >> (r0 + k) & 1 ? P::round(h) : P::zero());
+      }
+      out += kBatch * p.h.row;
+    }
+  }
+  store_some(p.last + state_at, bad, h);
+}
+
+// Their gradients, from the last row. space: a chunk of x, z and dh, and the rows' decays.
+template <typename T, bool TIED>
+__device__ __noinline__ void backward_again(const ScanParams& p, int b, int c0, uint32_t bad, uint8_t* space) {
+  using P = Pair<T>;
+  using Raw = typename P::Raw;
+  constexpr int R = kRowsOf<T>;
+  const int ch = c0 + 2 * lane_id(), n = min(max(p.D - ch, 0), 2), chunks = (p.L + R - 1) / R;
+  const size_t state_at = static_cast<size_t>(b) * p.D + ch;
+  Raw* xs = reinterpret_cast<Raw*>(space) + lane_id();
+  Raw* zs = xs + kRowsBytes / sizeof(Raw);
+  const Raw* ds = zs + kRowsBytes / sizeof(Raw);
+  uint64_t* ncs = reinterpret_cast<uint64_t*>(space + 3 * kRowsBytes) + lane_id();
+  Lane<T, false> lx(p.x, b, c0, p.D), lz(p.z, b, c0, p.D), ld(p.dh, b, c0, p.D);
+  lx.move((chunks - 1) * R), lz.move((chunks - 1) * R), ld.move((chunks - 1) * R);
+  ValidRows<R> valid(p, b);
+  valid.look((chunks - 1) * R);
+  uint64_t in = p.dlast ? load_state<false>(p.dlast + state_at, n) : 0ull;
+#pragma unroll 1
+  for (int c = chunks - 1; c >= 0; --c) {
+    const uint32_t bits = valid.take(c * R, (c - 1) * R);
+    fetch<T, false>(space, lx, false, bits, P::zero());
+    fetch<T, false>(space + kRowsBytes, lz, false, bits, P::inf());
+    fetch<T, false>(space + 2 * kRowsBytes, ld, false, p.dh.ptr ? bits : 0u, P::zero());
+    copies_commit();
+    lx.move(-R), lz.move(-R), ld.move(-R);
+    uint64_t h = load_state<false>(p.saved + (static_cast<size_t>(b) * chunks + c) * p.D + ch, n);
+    copies_wait<0>();
+    uint32_t zeros = 0;  // two bits a row: gates of zero
+#pragma unroll 1
+    for (int r0 = 0; r0 < R; r0 += kBatch) {
+      uint64_t z[kBatch], nc[kBatch], slope[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) z[k] = P::f32(zs[(r0 + k) * 32]);
+      neg_decay<T, false, true, true>(z, p.gate, nc, slope);
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int r = r0 + k;
+        const Raw x = xs[r * 32];
+        set_factor<T>(xs + r * 32, zs + r * 32, f2_mul(TIED ? f2_add(h, P::minus(x)) : h, slope[k]));
+        h = advance_any<T, TIED>(h, nc[k], gate_zero(z[k]), x);
+        ncs[r * 32] = nc[k];
+        zeros |= gate_zero(z[k]) << 2 * r;
+      }
+    }
+    T* dx = static_cast<T*>(p.dx.ptr) + b * p.dx.batch + (static_cast<long long>(c) * R + R - 1) * p.dx.row + ch;
+    T* dz = static_cast<T*>(p.dz.ptr) + b * p.dz.batch + (static_cast<long long>(c) * R + R - 1) * p.dz.row + ch;
+#pragma unroll 1
+    for (int r = R - 1; r >= 0; --r, dx -= p.dx.row, dz -= p.dz.row) {
+      const uint64_t nc = ncs[r * 32], q = get_factor<T>(xs + r * 32, zs + r * 32), g = f2_add(in, P::f32(ds[r * 32]));
+      in = decayed(g, nc, zeros >> 2 * r & 3u);
+      if (bits >> r & 1) {  // padded rows and those past the end are as they should be
+        store_some<T>(dx, bad, P::round(input_grad<TIED>(nc, g)));
+        store_some<T>(dz, bad, P::round(f2_mul(g, q)));
+      }
+    }
+  }
+  if (p.dh0) store_some(p.dh0 + state_at, bad, in);
+}
+
 // ---------------------------------------------------------------- forward, rows split over a cluster
 // Every step takes cluster x kWarps chunks. The next step's gates and local results are made between
 // sending a step's joins and waiting for the other blocks'.
@@ -529,7 +696,7 @@ constexpr int kSlots = 2 * 32 * sizeof(Join);  // what one block of a cluster se
 constexpr int kForwardRows = kWarps * 3 * 2 * kRowsBytes;  // three steps: two used, one on its way
 
 template <typename T, bool VEC, bool TAU1, bool TIED>
-__global__ void __launch_bounds__(kWarps * 32, 1) scan_forward_kernel(const ScanParams p) {
+__global__ void __launch_bounds__(kWarps * 32, 1) scan_forward_kernel(const __grid_constant__ ScanParams p) {
   using P = Pair<T>;
   using Raw = typename P::Raw;
   constexpr int R = kRowsOf<T>, kRows = kWarps * R;
@@ -612,7 +779,14 @@ __global__ void __launch_bounds__(kWarps * 32, 1) scan_forward_kernel(const Scan
     now = next;
     next = after;
   }
-  if (rank == 0 && w == 0) store_state<VEC>(p.last + state_at, n, carry);
+  const bool ends = rank == 0 && w == 0;
+  const uint32_t bad = not_finite(carry, n);  // the same in every warp of the cluster: all have joined the same values
+  if (ends && !bad) store_state<VEC>(p.last + state_at, n, carry);
+  if (ends && bad) store_some(p.last + state_at, ~bad & ((1u << n) - 1u), carry);
+  if (__any_sync(~0u, bad)) {
+    cluster_sync();  // every block's rows are stored
+    if (ends) forward_again<T, TIED>(p, b, c0, bad, dynamic);
+  }
 }
 
 // ---------------------------------------------------------------- forward, one block per tile
@@ -627,7 +801,7 @@ constexpr int kRelay = 12;  // warps of a block
 constexpr int kRelayShared = kRelay * 2 * 2 * kRowsBytes;
 
 template <typename T, bool VEC, bool TAU1, bool TIED>
-__global__ void __launch_bounds__(kRelay * 32, 2) scan_relay_kernel(const ScanParams p) {
+__global__ void __launch_bounds__(kRelay * 32, 2) scan_relay_kernel(const __grid_constant__ ScanParams p) {
   using P = Pair<T>;
   using Raw = typename P::Raw;
   constexpr int R = kRowsOf<T>;
@@ -658,7 +832,7 @@ __global__ void __launch_bounds__(kRelay * 32, 2) scan_relay_kernel(const ScanPa
     copies_commit();
     return bits;
   };
-  uint32_t now = start(w, 0);
+  uint32_t now = start(w, 0), bad = 0;
   for (int c = w, slot = 0; c < chunks; c += kRelay, slot ^= 1) {
     const uint32_t next = start(c + kRelay, slot ^ 1);
     copies_wait<1>();
@@ -686,7 +860,9 @@ __global__ void __launch_bounds__(kRelay * 32, 2) scan_relay_kernel(const ScanPa
       baton[to][lane] = end;
       relay_pass(to);
     } else {
-      store_state<VEC>(p.last + state_at, n, end);
+      bad = not_finite(end, n);
+      if (!bad) store_state<VEC>(p.last + state_at, n, end);
+      else store_some(p.last + state_at, ~bad & ((1u << n) - 1u), end);
     }
     if (saved) {
       store_state<VEC>(saved, n, h);
@@ -703,6 +879,7 @@ __global__ void __launch_bounds__(kRelay * 32, 2) scan_relay_kernel(const ScanPa
     __syncwarp();
     now = next;
   }
+  if (__syncthreads_or(bad) && __any_sync(~0u, bad)) forward_again<T, TIED>(p, b, c0, bad, dynamic);
 }
 
 // ---------------------------------------------------------------- backward
@@ -710,9 +887,10 @@ __global__ void __launch_bounds__(kRelay * 32, 2) scan_relay_kernel(const ScanPa
 // everything but g is independent of the other chunks: per row -c and
 // q = (h_{t-1} - [tied] x_t) a_t (1 - sigmoid(z_t)) / tau. Then, down the rows,
 // g_t = dh_t + in, dz_t = g_t q_t, in = a_t g_t. q takes the place of x and z in shared
-// memory (with -c and q of 16 rows in registers, 64 of them, the kernels spilled).
+// memory (with -c and q of 16 rows in registers, 64 of them, the kernels spilled). Returns the state
+// after the rows.
 template <typename T, bool TAU1, bool TIED>
-__device__ __forceinline__ void row_factors(typename Pair<T>::Raw* xs, typename Pair<T>::Raw* zs, uint64_t h,
+__device__ __forceinline__ uint64_t row_factors(typename Pair<T>::Raw* xs, typename Pair<T>::Raw* zs, uint64_t h,
                                             const DecayParams& gate, uint64_t (&nc)[kRowsOf<T>]) {
   using P = Pair<T>;
   constexpr int R = kRowsOf<T>;
@@ -730,42 +908,28 @@ __device__ __forceinline__ void row_factors(typename Pair<T>::Raw* xs, typename 
         const uint64_t q = f2_mul(TIED ? f2_add(h, P::minus(x)) : h, slope[k]);
         h = advance<T, TIED>(h, v[k], x);
         nc[r] = v[k];
-        if constexpr (sizeof(T) == 4) {
-          xs[r * 32] = q;
-        } else {
-          const float2 f = f2_unpack(q);
-          xs[r * 32] = __float_as_uint(f.x);
-          zs[r * 32] = __float_as_uint(f.y);
-        }
+        set_factor<T>(xs + r * 32, zs + r * 32, q);
       }
     }
   };
   if (any_far<T, TAU1, R>(zs, gate)) rows(std::true_type{});
   else rows(std::false_type{});
+  return h;
 }
-template <typename T>
-__device__ __forceinline__ uint64_t get_factor(const typename Pair<T>::Raw* xs, const typename Pair<T>::Raw* zs) {
-  if constexpr (sizeof(T) == 4) return *xs;
-  else return f2_pack(__uint_as_float(*xs), __uint_as_float(*zs));
-}
-template <bool TIED>
-__device__ __forceinline__ uint64_t input_grad(uint64_t nc, uint64_t g) {
-  return TIED ? f2_neg(f2_mul(nc, g)) : g;
-}
-
 // One block per tile, as the forward, with the chunks from the last and the relay going that
 // way: a chunk hands down out = P in + G.
 constexpr int kBackRelay = 8;
 constexpr int kBackRelayShared = kBackRelay * 2 * 3 * kRowsBytes;
 
 template <typename T, bool VEC, bool TAU1, bool TIED>
-__global__ void __launch_bounds__(kBackRelay * 32, 2) scan_relay_backward_kernel(const ScanParams p) {
+__global__ void __launch_bounds__(kBackRelay * 32, 2) scan_relay_backward_kernel(const __grid_constant__ ScanParams p) {
   using P = Pair<T>;
   using Raw = typename P::Raw;
   constexpr int R = kRowsOf<T>;
   constexpr uint32_t kFull = (1u << R) - 1u;
   extern __shared__ __align__(128) uint8_t dynamic[];
   __shared__ uint64_t baton[kBackRelay][32];
+  __shared__ uint32_t last_bad[32];  // lanes' channels whose last state is not finite
   const int w = warp_id(), lane = lane_id(), b = blockIdx.y, c0 = blockIdx.x * 64;
   const int ch = c0 + 2 * lane, n = min(max(p.D - ch, 0), 2);
   const int chunks = (p.L + R - 1) / R;
@@ -793,7 +957,7 @@ __global__ void __launch_bounds__(kBackRelay * 32, 2) scan_relay_backward_kernel
     copies_commit();
     return bits;
   };
-  uint32_t now = start(chunks - 1 - w, 0);
+  uint32_t now = start(chunks - 1 - w, 0), bad = 0;
   for (int c = chunks - 1 - w, slot = 0; c >= 0; c -= kBackRelay, slot ^= 1) {
     const uint64_t before = state;
     const uint32_t next = start(c - kBackRelay, slot ^ 1);
@@ -804,7 +968,8 @@ __global__ void __launch_bounds__(kBackRelay * 32, 2) scan_relay_backward_kernel
     Raw* zs = xs + kRowsBytes / sizeof(Raw);
     const Raw* ds = zs + kRowsBytes / sizeof(Raw);
     uint64_t nc[R];
-    row_factors<T, TAU1, TIED>(xs, zs, before, p.gate, nc);
+    const uint64_t after = row_factors<T, TAU1, TIED>(xs, zs, before, p.gate, nc);
+    if (c == chunks - 1) last_bad[lane] = not_finite(after, n);
     Join join{f2_both(1.f), 0ull};
 #pragma unroll
     for (int r = R - 1; r >= 0; --r) {
@@ -824,8 +989,12 @@ __global__ void __launch_bounds__(kBackRelay * 32, 2) scan_relay_backward_kernel
       const int to = w + 1 == kBackRelay ? 0 : w + 1;
       baton[to][lane] = end;
       relay_pass(to);
-    } else if (p.dh0) {
-      store_state<VEC>(p.dh0 + state_at, n, end);
+    } else {
+      bad = not_finite(end, n) | last_bad[lane];
+      if (p.dh0) {
+        if (!bad) store_state<VEC>(p.dh0 + state_at, n, end);
+        else store_some(p.dh0 + state_at, ~bad & ((1u << n) - 1u), end);
+      }
     }
 #pragma unroll
     for (int r = R - 1; r >= 0; --r) {
@@ -843,6 +1012,7 @@ __global__ void __launch_bounds__(kBackRelay * 32, 2) scan_relay_backward_kernel
     __syncwarp();
     now = next;
   }
+  if (__syncthreads_or(bad) && __any_sync(~0u, bad)) backward_again<T, TIED>(p, b, c0, bad, dynamic);
 }
 
 // Rows split over a cluster, as in the forward: rank 0 and its warp 0 take the latest chunks.
@@ -850,12 +1020,13 @@ constexpr int kBackWarps = 11;  // three steps of x, z and dh fill the shared me
 constexpr int kBackRows = kBackWarps * 3 * 3 * kRowsBytes;
 
 template <typename T, bool VEC, bool TAU1, bool TIED>
-__global__ void __launch_bounds__(kBackWarps * 32, 1) scan_backward_kernel(const ScanParams p) {
+__global__ void __launch_bounds__(kBackWarps * 32, 1) scan_backward_kernel(const __grid_constant__ ScanParams p) {
   using P = Pair<T>;
   using Raw = typename P::Raw;
   constexpr int R = kRowsOf<T>;
   extern __shared__ __align__(128) uint8_t dynamic[];
   __shared__ Join warps[2][kBackWarps][32];
+  __shared__ uint32_t last_bad[32];  // lanes' channels whose last state is not finite
   const int cluster = p.cluster, rank = cluster > 1 ? cluster_ctarank() : 0;
   const int w = warp_id(), lane = lane_id(), b = blockIdx.y;
   const int c0 = blockIdx.x / cluster * 64, ch = c0 + 2 * lane, n = min(max(p.D - ch, 0), 2);
@@ -895,7 +1066,7 @@ __global__ void __launch_bounds__(kBackWarps * 32, 1) scan_backward_kernel(const
     copies_wait<1>();
     __syncwarp();
     Raw* xs = rows_of(step);
-    row_factors<T, TAU1, TIED>(xs, xs + kTensor, state, p.gate, nc);
+    const uint64_t after = row_factors<T, TAU1, TIED>(xs, xs + kTensor, state, p.gate, nc);
     Join join{f2_both(1.f), 0ull};
 #pragma unroll
     for (int r = R - 1; r >= 0; --r) {
@@ -904,13 +1075,16 @@ __global__ void __launch_bounds__(kBackWarps * 32, 1) scan_backward_kernel(const
       join.p = f2_fma(nc[r], join.p, join.p);
     }
     warps[step & 1][w][lane] = join;
+    return after;
   };
 
   Step now = start_step(0), next = start_step(1);
   uint64_t carry = p.dlast ? load_state<VEC>(p.dlast + state_at, n) : 0ull;
   if (cluster > 1) cluster_sync();
   uint64_t nc[R], nc_next[R];
-  local(0, now.state, nc);
+  const uint32_t state_bad = not_finite(local(0, now.state, nc), n);
+  if (rank == 0 && w == 0)  // it has the sequence's last state; sent to the blocks with the first step's joins
+    for (int r = 0; r < cluster; ++r) st_cluster_u32(mapa_shared(smem_u32(last_bad + lane), r), state_bad);
   for (int step = 0; step < steps; ++step) {
     const int c = last - step * each;
     __syncthreads();
@@ -950,7 +1124,14 @@ __global__ void __launch_bounds__(kBackWarps * 32, 1) scan_backward_kernel(const
     now = next;
     next = after;
   }
-  if (p.dh0 && rank == 0 && w == 0) store_state<VEC>(p.dh0 + state_at, n, carry);
+  const bool ends = rank == 0 && w == 0;
+  const uint32_t bad = not_finite(carry, n) | last_bad[lane];  // the same in every warp of the cluster, as in the forward
+  if (p.dh0 && ends && !bad) store_state<VEC>(p.dh0 + state_at, n, carry);
+  if (p.dh0 && ends && bad) store_some(p.dh0 + state_at, ~bad & ((1u << n) - 1u), carry);
+  if (__any_sync(~0u, bad)) {
+    cluster_sync();  // every block's rows are stored
+    if (ends) backward_again<T, TIED>(p, b, c0, bad, dynamic);
+  }
 }
 
 // ---------------------------------------------------------------- single tokens
@@ -967,7 +1148,7 @@ __global__ void __launch_bounds__(128) scan_step_kernel(const StepParams p) {
     const uint64_t zz[1] = {z};
     uint64_t nc[1], unused[1];
     neg_decay<T, TAU1, true, false>(zz, p.gate, nc, unused);
-    const uint64_t h = advance<T, TIED>(load_state<VEC>(s, n), nc[0], x);
+    const uint64_t h = advance_any<T, TIED>(load_state<VEC>(s, n), nc[0], gate_zero(z), x);
     store_state<VEC>(s, n, h);
     out = P::round(h);
   }

@@ -273,7 +273,7 @@ def gated_scan(x, gate, *, mask=None, initial_state=None, gate_normalizer: float
     """The gated recurrence: (h [B, L, D], last_state float32 [B, D]).
 
     x, gate         [B, L, D]; gate holds logits: a_t = sigmoid(gate_t) ** (1 / gate_normalizer).
-                    A logit of -inf empties the state before its token.
+                    A logit of -inf empties a finite state before its token (an infinite one: NaN).
     mask            optional valid tokens [B, L] (bool or uint8, nonzero = valid): a padded token
                     leaves the state as it is, its output is zero and its row is not read.
     initial_state   optional float32 [B, D] (default zeros); pass a call's last_state to go on.

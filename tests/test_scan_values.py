@@ -70,3 +70,109 @@ def test_slopes_of_gates_that_forget(L, at, tau, dtype):
         err = U * (2 * np.abs(host(z)[0, at]) + 6 * s + 24) * np.abs(want[0, at])
         near(torch.from_numpy(dz[0, at]), want[0, at], err, dtype)
         assert not dz[0, M[0].numpy() == 0].any()
+
+
+def same_values(got, want, dtype, err=1e-5):
+    """The same infinities and NaN, and finite values within half a step and err of the largest."""
+    got, half = host(got), 0.0 if dtype == F32 else torch.finfo(dtype).eps / 2
+    assert np.array_equal(np.isnan(got), np.isnan(want))
+    assert np.array_equal(np.isposinf(got), np.isposinf(want)) and np.array_equal(np.isneginf(got), np.isneginf(want))
+    f = np.isfinite(want)
+    if f.any():
+        scale = np.abs(want[f]).max()
+        assert (np.abs(got[f] - want[f]) <= half * np.abs(want[f]) + err * scale).all()
+
+
+@pytest.mark.parametrize("tied", [False, True])
+@pytest.mark.parametrize("tau", [1.0, 16.0])
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("mask", [None, "random"])
+@pytest.mark.parametrize("B,L,D", FORMS + [(2, 130, 33), (1, 16, 2), (1, 1, 1)])
+def test_infinite_inputs_and_states(B, L, D, mask, dtype, tau, tied):
+    """a h + u of an infinite h is infinite: such a state stays what it is over gates and padded rows, until an
+    infinity of the other sign or a gate of zero makes it NaN. The other channels keep their bits."""
+    from scale_gated_linear_b200 import gated_scan, gated_scan_backward, gated_scan_forward
+    x, z, M, h0, dh, dlast = inputs(B, L, D, dtype, bias=1.0, mask=mask, state=True, seed=L)
+    if M is not None:
+        M[:, L // 3] = 1
+    clean = [None if t is None else t.cuda() for t in (x, z, M, h0, dh, dlast)]
+    kw = dict(tied=tied, gate_normalizer=tau)
+    inf = float("inf")
+    x, z, h0, dh, dlast = (t.clone() for t in (x, z, h0, dh, dlast))
+    x[0, L // 3, 0] = inf
+    h0[-1, D // 2] = -inf
+    dh[0, L // 3, D - 1] = -inf
+    dlast[-1, D // 3] = inf
+    if D > 8 and L > 8:
+        x[0, L // 3, 5], x[0, L // 2, 5] = inf, -inf        # NaN from the second on, where it is valid
+        x[0, L // 3, 6], z[0, L // 2, 6] = -inf, -inf       # a gate of zero: 0 * inf
+        x[0, L // 3, 7] = float("nan")
+    cu = [None if t is None else t.cuda() for t in (x, z, M, h0, dh, dlast)]
+
+    def both(x, z, M, h0, dh, dlast):
+        h, last, saved = gated_scan_forward(x, z, mask=M, initial_state=h0, **kw)
+        h2, last2 = gated_scan(x, z, mask=M, initial_state=h0, **kw)
+        for a, b in ((h, h2), (last, last2)):
+            assert torch.equal(a.nan_to_num(7.0), b.nan_to_num(7.0))
+        return (h, last, *gated_scan_backward(dh, dlast, saved))
+
+    got, before = both(*cu), both(*clean)
+    m = None if M is None else M.numpy()
+    with np.errstate(invalid="ignore"):
+        args = (host(x), host(z), tau, tied, m, host(h0))
+        want = (*oo.scan(*args)[:2], *oo.scan_backward(host(dh), host(dlast), *args)[:3])
+    for k, (a, w) in enumerate(zip(got, want)):
+        same_values(a, w, F32 if k in (1, 4) else dtype)
+    touched = torch.zeros(B, D, dtype=torch.bool)
+    touched[0, [0, D - 1]] = True
+    touched[-1, [D // 2, D // 3]] = True
+    if D > 8 and L > 8:
+        touched[0, 5:8] = True
+    for a, b in zip(got, before):
+        keep = ~touched if a.dim() == 2 else ~touched[:, None].expand(B, L, D)
+        assert torch.equal(a.cpu()[keep], b.cpu()[keep])
+
+
+def test_infinite_states_in_place():
+    """The state taken on in its own buffer, as the C entry allows, with an infinity in it."""
+    import ctypes
+    from scale_gated_linear_b200 import _lib, gated_scan_backward, gated_scan_forward
+    lib = _lib.load()
+    for B, L, D in FORMS:
+        x, z, _, h0, dh, dlast = (None if t is None else t.cuda() for t in inputs(B, L, D, F32, state=True, seed=2))
+        h0[0, 3], dlast[0, 5] = float("inf"), float("-inf")
+        cfg = _lib.ScanConfig(0, 2, D, 0, 16.0)
+        rows = lambda t: _lib.Rows(t.data_ptr(), L * D, D)
+        want, wlast, saved = gated_scan_forward(x, z, initial_state=h0)
+        h, state, kept = torch.empty_like(x), h0.clone(), torch.empty_like(saved.states)
+        st = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        _lib.check(lib.msgla_scan_forward(cfg, B, L, rows(x), rows(z), None, state.data_ptr(), rows(h), state.data_ptr(),
+                                          kept.data_ptr(), st))
+        assert torch.equal(h, want) and torch.equal(state, wlast) and torch.equal(kept, saved.states)
+        assert state[0, 3] == float("inf") and torch.isinf(state).sum() == 1
+        dx, dz, grad = torch.empty_like(x), torch.empty_like(x), dlast.clone()
+        _lib.check(lib.msgla_scan_backward(cfg, B, L, rows(x), rows(z), None, kept.data_ptr(), rows(dh), grad.data_ptr(),
+                                           rows(dx), rows(dz), grad.data_ptr(), st))
+        torch.cuda.synchronize()
+        for a, b in zip((dx, dz, grad), gated_scan_backward(dh, dlast, saved)):
+            assert torch.equal(a.nan_to_num(7.0), b.nan_to_num(7.0))
+        assert grad[0, 5] == float("-inf") and torch.isinf(grad).sum() == 1 and not torch.isnan(grad).any()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("tau", [1.0, 16.0])
+def test_step_of_infinite_states(tau, dtype):
+    from scale_gated_linear_b200 import gated_scan_step
+    B, D = 3, 40
+    x, z, _, h0, _, _ = inputs(B, 1, D, dtype, state=True, seed=5)
+    inf = float("inf")
+    h0[0, 0], h0[1, 1], h0[2, 2], h0[0, 3], x[0, 0, 4], x[1, 0, 1] = inf, -inf, inf, inf, -inf, inf
+    z[0, 0, 3] = -inf
+    M = torch.tensor([1, 1, 0], dtype=torch.uint8)
+    for tied in (False, True):
+        state = h0.cuda()
+        h = gated_scan_step(x[:, 0].cuda(), z[:, 0].cuda(), state, mask=M.cuda(), gate_normalizer=tau, tied=tied)
+        with np.errstate(invalid="ignore"):
+            want, last, _ = oo.scan(host(x), host(z), tau, tied, M.numpy()[:, None], host(h0))
+        same_values(h, want[:, 0], dtype)
+        same_values(state, last, F32)
