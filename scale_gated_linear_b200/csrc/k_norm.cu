@@ -900,6 +900,7 @@ struct HoldPlan {
   int shared;             // bytes
 };
 constexpr int kMaxHold = 8, kMaxHoldGroups = 32;
+constexpr int kHoldShared = 212 * 1024;  // most that a block asks for
 
 template <typename T, int V, int TENSORS>
 struct Hold {
@@ -1232,7 +1233,10 @@ bool hold_plan(const NormParams& p, int v, int tensors, HoldPlan& q) {
   long long data = rows * q.tx * 16 * tensors;
   const long long cells = static_cast<long long>(q.ty) * q.width * 8;
   if (tensors > 1 && data < cells) return false;  // the weights' sums take the place of x in the end
-  q.shared = static_cast<int>(data + kThreads * 8 + 2 * c * (q.groups + 1) * 8 + rows);
+  // with one or two vectors a row the rows' valid marks alone pass what 200 KB of rows leave
+  const long long shared = data + kThreads * 8 + 2 * c * (q.groups + 1) * 8 + rows;
+  if (shared > kHoldShared) return false;
+  q.shared = static_cast<int>(shared);
   return true;
 }
 
@@ -1304,7 +1308,7 @@ cudaError_t launch_after(void (*kernel)(KArgs...), dim3 grid, dim3 block, int sh
 
 template <auto kernel, typename... Args>
 cudaError_t launch_hold(const HoldPlan& q, const NormParams& p, cudaStream_t st, const Args&... args) {
-  cudaError_t e = allow_shared<kernel>(212 * 1024);
+  cudaError_t e = allow_shared<kernel>(kHoldShared);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.N * q.tiles * q.cluster));

@@ -1,0 +1,57 @@
+"""Group normalisation over sequences at the borders of its forms: samples held in the shared memory of
+a cluster up to the most that it holds, and larger ones in two passes, with 16-byte vectors."""
+import numpy as np
+import pytest
+
+from oracle import ops_oracle as oo
+
+torch = pytest.importorskip("torch")
+pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA device")]
+
+from test_group_norm import BF16, F16, F32, check, host, near  # noqa: E402
+
+# norm_error counts 192 roundings, for at most 96 additions in a row in one thread. A thread of the held
+# form adds up to 400 values (1600 rows of a block by 32 at once, 8 channels): 400 + 96 < 3 * 192.
+HELD = 3
+
+
+def compare(x, G, w, b, gate, mask, act, center, dy, eps, factor, dtype):
+    """Forward and backward on the GPU against the oracle; x [N, S, C]."""
+    from scale_gated_linear_b200 import group_norm_backward, group_norm_forward
+    cu = lambda t: None if t is None else t.cuda()
+    y, saved = group_norm_forward(x.cuda(), G, cu(w), cu(b), gate=cu(gate), mask=cu(mask), activation=act, eps=eps, center=center)
+    dx, dw, db, dg = group_norm_backward(dy.cuda(), saved)
+    args = dict(gate=host(gate), mask=None if mask is None else mask.numpy(), act=act, eps=eps, center=center, dy=host(dy))
+    wy, (wx, ww, wb, wg) = oo.group_norm(host(x), G, host(w), host(b), **args)
+    ey, (ex, ew, eb, eg) = oo.norm_error(host(x), G, host(w), host(b), **args)
+    near(y, wy, factor * ey, dtype)
+    near(dx, wx, factor * ex, dtype)
+    near(dw, ww, factor * ew, F32)
+    near(db, wb, factor * eb, F32)
+    if gate is not None:
+        near(dg, wg, factor * eg, dtype)
+
+
+@pytest.mark.parametrize("dtype,C", [(BF16, 8), (F16, 8), (F32, 4)])
+@pytest.mark.parametrize("S", [12635, 101072, 101073, 102400, 102401])
+def test_long_samples_of_one_vector(S, dtype, C):
+    """One vector a row: the valid marks of the rows take a sixteenth of the rows' own bytes, and samples
+    from about 10^5 rows on no longer fit a cluster."""
+    g = torch.Generator().manual_seed(S)
+    x, dy = (torch.randn(1, S, C, generator=g) * 2 + 0.5).to(dtype), torch.randn(1, S, C, generator=g).to(dtype)
+    w, b = 1 + 0.3 * torch.randn(C, generator=g), 0.3 * torch.randn(C, generator=g)
+    mask = (torch.rand(1, S, generator=g) < 0.9).to(torch.uint8) if S == 102400 else None
+    compare(x, 1, w, b, None, mask, "silu", True, dy, 1e-5, HELD, dtype)
+
+
+@pytest.mark.parametrize("N,S,C,G,dtype,gated,center", [
+    (1, 12000, 64, 1, BF16, False, True),   # about 190 KB a block forward, two passes backward
+    (1, 6200, 64, 4, BF16, False, True),    # the same backward
+    (1, 4100, 64, 2, F16, True, False),     # with a gate
+    (2, 6300, 32, 1, F32, False, False), (1, 3000, 32, 4, F32, True, True)])
+def test_held_near_the_limit(N, S, C, G, dtype, gated, center):
+    g = torch.Generator().manual_seed(S)
+    r = lambda *s: torch.randn(*s, generator=g)
+    x, dy, gate = (r(N, S, C) * 2 + 0.5).to(dtype), r(N, S, C).to(dtype), r(N, S, C).to(dtype) if gated else None
+    mask = (torch.rand(N, S, generator=g) < 0.8).to(torch.uint8)
+    compare(x, G, 1 + 0.3 * r(C), 0.3 * r(C), gate, mask, "silu", center, dy, 1e-5, HELD, dtype)
