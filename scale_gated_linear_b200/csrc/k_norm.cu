@@ -20,9 +20,9 @@
 // Measured, bf16: 65536 groups of 512 (16384 x 2048) under an output gate forward 37 us (82 % of copy
 // bandwidth), backward 73 and 6 for the weights (70 %); 8 x 2048 x 1024 in 32 groups with padding
 // 78 us forward and backward held in shared memory, 97 in two passes.
-// Variances are sums of squared differences: from the mean itself in registers, else from each
-// thread's first value, joined by count, mean and sum of squares, so that a mean far
-// from zero costs no digits. Everything is summed in f32 in a fixed order.
+// Variances are sums of squared differences: from the mean itself in registers; held, from a mean that
+// the sum of the differences corrects; in two passes from each thread's first value, joined by count, mean and
+// sum of squares. So a mean far from zero costs no digits. Everything is summed in f32 in a fixed order.
 #include <type_traits>
 
 #include "ops_internal.h"
@@ -1018,17 +1018,28 @@ __global__ void __launch_bounds__(kThreads, 4) norm_hold_forward_kernel(const No
         for (int e = 0; e < V; ++e) sum += f[e];
       }
   const float2 total = h.group_sum(make_float2(sum, 0.f), h.valid_rows(), 0, cg, count);
-  const float elements = fmaxf(count * cg, 1.f), mean = p.center ? total.x / elements : 0.f;
-  float squares = 0.f;
+  const float elements = fmaxf(count * cg, 1.f);
+  float mean = p.center ? total.x / elements : 0.f;
+  const uint64_t minus = f2_pack(-mean, -mean);
+  uint64_t off = 0, squares = 0;
   if (h.here)
     for (int row = h.ty; row < h.rows; row += q.ty)
       if (h.valid[row]) {
         float f[V];
         h.get(0, row, f);
 #pragma unroll
-        for (int e = 0; e < V; ++e) squares = fmaf(f[e] - mean, f[e] - mean, squares);
+        for (int e = 0; e < V; e += 2) {
+          const uint64_t d = f2_add(f2_pack(f[e], f[e + 1]), minus);
+          off = f2_add(off, d);
+          squares = f2_fma(d, d, squares);
+        }
       }
-  const float rstd = 1.f / sqrtf(h.group_sum(make_float2(squares, 0.f), 0.f, 1, cg, count).x / elements + p.eps);
+  // the sum of up to 400 values a thread left the mean off by a few of its steps, which the differences show
+  const float2 o = f2_unpack(off), sq = f2_unpack(squares);
+  float2 about = h.group_sum(make_float2(o.x + o.y, sq.x + sq.y), 0.f, 1, cg, count);
+  about.x = p.center ? about.x / elements : 0.f;
+  mean += about.x;
+  const float rstd = 1.f / sqrtf(fmaxf(about.y / elements - about.x * about.x, 0.f) + p.eps);
   if (!h.here) return;
   if (p.stats && h.rank == 0 && h.ty == 0 && h.c % cg == 0)
     *reinterpret_cast<float2*>(p.stats + 2 * (h.n * p.G + h.c / cg)) = make_float2(mean, rstd);

@@ -47,11 +47,6 @@ constexpr float kLog2e = 1.4426950408889634f, kLog2eLow = 1.4426950408889634 - s
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kMaxCluster = 8;
 
-__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
 __device__ __forceinline__ uint64_t f2_both(float v) { return f2_pack(v, v); }
 __device__ __forceinline__ uint64_t f2_neg(uint64_t a) { return a ^ 0x8000000080000000ull; }
 __device__ __forceinline__ float rcp_approx(float x) {

@@ -55,3 +55,30 @@ def test_held_near_the_limit(N, S, C, G, dtype, gated, center):
     x, dy, gate = (r(N, S, C) * 2 + 0.5).to(dtype), r(N, S, C).to(dtype), r(N, S, C).to(dtype) if gated else None
     mask = (torch.rand(N, S, generator=g) < 0.8).to(torch.uint8)
     compare(x, G, 1 + 0.3 * r(C), 0.3 * r(C), gate, mask, "silu", center, dy, 1e-5, HELD, dtype)
+
+
+@pytest.mark.parametrize("center", [True, False])
+@pytest.mark.parametrize("N,S,C,G", [(2, 4096, 64, 1), (1, 16384, 8, 1), (1, 1000, 256, 8), (2, 14000, 64, 1), (2, 300, 2048, 1)])
+def test_constant_samples(N, S, C, G, center):
+    """No variance: y = bias to the bit, though 300.1 does not add up exactly. A mean that is off by a few of
+    its own steps would give (x - mean)^2 far above this eps. Not centred: one to within 600 roundings."""
+    from scale_gated_linear_b200 import group_norm
+    b = torch.randn(C, device="cuda")
+    y = group_norm(torch.full((N, S, C), 300.1, device="cuda"), G, None, b, eps=1e-12, center=center)
+    if center:
+        assert torch.equal(y, b.expand(N, S, C))
+    else:
+        assert (y - b - 1).abs().max() <= 600 * 2.0 ** -24 * (1 + 2 * b.abs().max())
+
+
+@pytest.mark.parametrize("N,S,C,G", [(2, 4096, 64, 1), (1, 16384, 8, 1), (1, 1000, 256, 8), (2, 14000, 64, 1), (2, 300, 2048, 1)])
+def test_far_mean(N, S, C, G):
+    """A mean of 300 standard deviations in samples of many rows. The mean may be rounded by U |mean| some 24
+    times (blocks of rows are joined by their means, in fewer than 20 steps), beside the sums' roundings of
+    values of order one."""
+    from scale_gated_linear_b200 import group_norm
+    g = torch.Generator().manual_seed(C)
+    x = torch.randn(N, S, C, generator=g) + 300
+    want = oo.group_norm(host(x), G)
+    err = 2.0 ** -24 * (24 * 301 + 3 * 192 * (1 + np.abs(want)))
+    near(group_norm(x.cuda(), G), want, err, F32)
