@@ -1155,12 +1155,6 @@ __global__ void __launch_bounds__(kThreads, GATED ? 2 : 3) norm_hold_backward_ke
 }
 
 // ---------------------------------------------------------------- plans and launches
-int multiprocessors() {
-  int dev = 0, n = 148;
-  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-  return n;
-}
-
 bool aligned16(const Rows& r, int dtype) {
   const int run = dtype == kF32 ? 4 : 8;
   return !r.ptr || (reinterpret_cast<uintptr_t>(r.ptr) % 16 == 0 && r.batch % run == 0 && r.row % run == 0);
@@ -1190,7 +1184,7 @@ RowPlan row_plan(const NormParams& p, int v, int per_sm) {
   q.rpi = teams / q.gs;
   q.slices = (p.G + q.gs - 1) / q.gs;
   const long long most = (p.N + q.rpi - 1) / q.rpi;
-  const long long want = (static_cast<long long>(multiprocessors()) * per_sm + q.slices - 1) / q.slices;
+  const long long want = (static_cast<long long>(p.sms) * per_sm + q.slices - 1) / q.slices;
   q.blocks = static_cast<int>(most < want ? most : want);
   if (q.blocks > 65535) q.blocks = 65535;
   return q;
@@ -1208,7 +1202,7 @@ BlockPlan block_plan(const NormParams& p, int v, int per_sm) {
   q.width = q.tx * v;
   q.tiles = (p.C + q.width - 1) / q.width;
   const long long blocks = p.N * q.tiles, rows_at_once = (p.S + q.ty - 1) / q.ty;
-  long long chunks = static_cast<long long>(per_sm) * multiprocessors() / blocks;
+  long long chunks = static_cast<long long>(per_sm) * p.sms / blocks;
   const long long least = (rows_at_once + 63) / 64, most = rows_at_once < 512 ? rows_at_once : 512;
   if (chunks < least) chunks = least;
   if (chunks > most) chunks = most;
@@ -1236,7 +1230,7 @@ bool hold_plan(const NormParams& p, int v, int tensors, HoldPlan& q) {
   const long long bytes = p.S * q.tx * 16 * tensors, units = p.N * q.tiles;
   long long c = (bytes + 48 * 1024 - 1) / (48 * 1024);
   if (c > kMaxHold) c = kMaxHold;
-  while (c < kMaxHold && units * c < 2LL * multiprocessors() && p.S / (c + 1) >= 2 * q.ty) ++c;
+  while (c < kMaxHold && units * c < 2LL * p.sms && p.S / (c + 1) >= 2 * q.ty) ++c;
   const long long rows = (p.S + c - 1) / c;
   if (rows * q.tx * 16 * tensors > 200 * 1024 || units * c > 0x7fffffffLL) return false;
   q.rows = static_cast<int>(rows);

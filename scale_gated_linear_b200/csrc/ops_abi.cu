@@ -144,7 +144,16 @@ int check_norm(const msgla_norm_config* c, long long N, long long S) {
   return MSGLA_OK;
 }
 
-NormParams norm_params(const msgla_norm_config* c, long long N, long long S) {
+// The SMs of device `dev` (148 where no GPU can be asked, so that sizes can be made there).
+int count_sms(int dev, int* sms) {
+  const cudaError_t e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess) return MSGLA_OK;
+  if (e == cudaErrorInvalidDevice) return cuda_error(e, "asking for the device");
+  *sms = 148;
+  return MSGLA_OK;
+}
+
+int norm_params(const msgla_norm_config* c, long long N, long long S, NormParams* to) {
   NormParams p = {};
   p.dtype = c->dtype;
   p.C = c->C;
@@ -154,7 +163,8 @@ NormParams norm_params(const msgla_norm_config* c, long long N, long long S) {
   p.eps = c->eps;
   p.N = N;
   p.S = S;
-  return p;
+  *to = p;
+  return count_sms(c->device, &to->sms);
 }
 
 int check_workspace(const NormParams& p, bool backward, void* ws, size_t bytes, Spans& spans) {
@@ -282,7 +292,9 @@ int msgla_group_norm_workspace_size(const msgla_norm_config* cfg, long long N, l
                                     size_t* bytes) {
   TRY(check_norm(cfg, N, S));
   if (!bytes) return set_error(MSGLA_ERR_INVALID_ARG, "bytes is NULL");
-  *bytes = N * S == 0 ? 0 : norm_workspace(norm_params(cfg, N, S), gradients != 0);
+  NormParams p;
+  TRY(norm_params(cfg, N, S, &p));
+  *bytes = N * S == 0 ? 0 : norm_workspace(p, gradients != 0);
   return MSGLA_OK;
 }
 
@@ -295,7 +307,8 @@ int msgla_group_norm_forward(const msgla_norm_config* cfg, long long N, long lon
   TRY(take_f32("weight", weight, false));
   TRY(take_f32("bias", bias, false));
   if (reinterpret_cast<uintptr_t>(stats) % 8) return set_error(MSGLA_ERR_INVALID_ARG, "stats is not 8-byte aligned");
-  NormParams p = norm_params(cfg, N, S);
+  NormParams p;
+  TRY(norm_params(cfg, N, S, &p));
   Spans spans;
   TRY(take_rows("x", x, N, S, cfg->C, cfg->dtype, false, spans, &p.x));
   if (gate) TRY(take_rows("gate", gate, N, S, cfg->C, cfg->dtype, false, spans, &p.gate));
@@ -335,7 +348,8 @@ int msgla_group_norm_backward(const msgla_norm_config* cfg, long long N, long lo
   if (!stats || reinterpret_cast<uintptr_t>(stats) % 8)
     return set_error(MSGLA_ERR_INVALID_ARG, "stats is NULL or not 8-byte aligned");
   if (!gate != !dgate) return set_error(MSGLA_ERR_INVALID_ARG, "gate and dgate go together");
-  NormParams p = norm_params(cfg, N, S);
+  NormParams p;
+  TRY(norm_params(cfg, N, S, &p));
   Spans spans;
   TRY(take_rows("x", x, N, S, cfg->C, cfg->dtype, false, spans, &p.x));
   if (gate) TRY(take_rows("gate", gate, N, S, cfg->C, cfg->dtype, false, spans, &p.gate));

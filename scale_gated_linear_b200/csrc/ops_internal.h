@@ -62,6 +62,7 @@ cudaError_t launch_scan_step(const StepParams& p, cudaStream_t st);
 // ---------------------------------------------------------------- group normalisation
 struct NormParams {
   int dtype, C, G, act, center;
+  int sms;  // of the call's device: the plans, and with them the workspace, depend on it
   float eps;
   long long N, S;
   Rows x, gate, y, dy, dx, dgate;  // gate.ptr null: no gate
