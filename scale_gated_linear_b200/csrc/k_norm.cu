@@ -1368,7 +1368,8 @@ cudaError_t launch_norm_forward(const NormParams& p, cudaStream_t st) {
     if (rows_form(p, v)) {
       const RowPlan q = row_plan(p, v, kRowBlocks);
       by_vectors<V>(p, q, [&](auto nv, auto team) {
-        norm_rows_forward_kernel<T, V, decltype(nv)::value, decltype(team)::value><<<dim3(q.slices, q.blocks), kThreads, 0, st>>>(p, q);
+        e = launch_plain(norm_rows_forward_kernel<T, V, decltype(nv)::value, decltype(team)::value>, dim3(q.slices, q.blocks),
+                         dim3(kThreads), 0, st, p, q);
       });
     } else if (HoldPlan hold; hold_plan(p, v, 1, hold)) {
       if constexpr (V > 1) e = launch_hold<norm_hold_forward_kernel<T, V>>(hold, p, st, p, hold);
@@ -1380,12 +1381,13 @@ cudaError_t launch_norm_forward(const NormParams& p, cudaStream_t st) {
         e = cudaErrorInvalidConfiguration;
         return;
       }
-      norm_sums_kernel<T, V><<<unsigned(grid), kThreads, 0, st>>>(p, q, s.seg, s.rows_of);
+      e = launch_plain(norm_sums_kernel<T, V>, dim3(unsigned(grid)), dim3(kThreads), 0, st, p, q, s.seg, s.rows_of);
+      if (e != cudaSuccess) return;
       e = launch_after(norm_apply_kernel<T, V>, dim3(unsigned(grid)), dim3(kThreads), (q.width + 1) * 8, st, p, q,
                        static_cast<const float2*>(s.seg), static_cast<const float*>(s.rows_of));
     }
   });
-  return e == cudaSuccess ? cudaGetLastError() : e;
+  return e;
 }
 
 cudaError_t launch_norm_backward(const NormParams& p, cudaStream_t st) {
@@ -1403,7 +1405,8 @@ cudaError_t launch_norm_backward(const NormParams& p, cudaStream_t st) {
         constexpr int kRows = kAhead * kRowStage<T, V, decltype(nv)::value>, kSums = kThreads * V * decltype(nv)::value * 8;
         constexpr int kShared = kRows > kSums ? kRows : kSums;
         e = allow_shared<kernel>(kShared);
-        if (e == cudaSuccess) kernel<<<dim3(q.slices, q.blocks), kThreads, kRows > sums ? kRows : sums, st>>>(p, q);
+        if (e == cudaSuccess)
+          e = launch_plain(kernel, dim3(q.slices, q.blocks), dim3(kThreads), kRows > sums ? kRows : sums, st, p, q);
       });
       if (e == cudaSuccess) e = launch_weights(p, static_cast<const float*>(p.workspace), q.blocks, st);
     } else if (HoldPlan hold; hold_plan(p, v, p.gate.ptr ? 3 : 2, hold)) {
@@ -1421,13 +1424,15 @@ cudaError_t launch_norm_backward(const NormParams& p, cudaStream_t st) {
         e = cudaErrorInvalidConfiguration;
         return;
       }
-      norm_grad_sums_kernel<T, V><<<unsigned(grid), kThreads, kThreads * V * 8, st>>>(p, q, s.chan, s.seg, s.rows_of);
+      e = launch_plain(norm_grad_sums_kernel<T, V>, dim3(unsigned(grid)), dim3(kThreads), kThreads * V * 8, st, p, q, s.chan,
+                       s.seg, s.rows_of);
+      if (e != cudaSuccess) return;
       e = launch_after(norm_grad_apply_kernel<T, V>, dim3(unsigned(grid)), dim3(kThreads), (q.width + 1) * 8, st, p, q,
                        static_cast<const float2*>(s.seg), static_cast<const float*>(s.rows_of));
       if (e == cudaSuccess) e = launch_weights(p, s.chan, static_cast<int>(parts), st);
     }
   });
-  return e == cudaSuccess ? cudaGetLastError() : e;
+  return e;
 }
 
 }  // namespace msgla

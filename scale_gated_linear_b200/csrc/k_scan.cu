@@ -1196,7 +1196,10 @@ const int* clusters_at_once(const void* kernel, int threads, int shared) {
       cfg.attrs = attr;
       cfg.numAttrs = 1;
       int n = 0;
-      if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) n = 1;
+      if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
+        cudaGetLastError();  // the call's own launch is what reports an error
+        n = 1;
+      }
       table[dev][c] = n;
     }
   });
@@ -1324,10 +1327,12 @@ cudaError_t launch_scan_step(const StepParams& params, cudaStream_t st) {
   bool vec = p.D % 2 == 0 && aligned_state(p.state);
   for (const Rows& r : rows) vec = vec && aligned_rows(r, 2, p.dtype);
   const dim3 grid((p.D + 255) / 256, p.B);
+  cudaError_t e = cudaSuccess;
   by_kind(p.dtype, vec, p.inv_tau == 1.f, p.tied, [&](auto t, auto v, auto tau1, auto tied) {
-    scan_step_kernel<decltype(t), decltype(v)::value, decltype(tau1)::value, decltype(tied)::value><<<grid, 128, 0, st>>>(p);
+    e = launch_plain(scan_step_kernel<decltype(t), decltype(v)::value, decltype(tau1)::value, decltype(tied)::value>, grid,
+                     dim3(128), 0, st, p);
   });
-  return cudaGetLastError();
+  return e;
 }
 
 }  // namespace msgla

@@ -11,23 +11,27 @@ using namespace msgla;
 
 namespace {
 
+// Reported by this call, and so taken out of the thread's last error: no later call finds it there.
+int cuda_error(cudaError_t e, const char* what) {
+  cudaGetLastError();
+  return set_error(MSGLA_ERR_CUDA, "%s failed: %s", what, cudaGetErrorString(e));
+}
+
 // Makes `dev` the current device for a call, and the previous one again.
 struct Device {
   int prev = -1;
-  bool ok = false, moved = false;
+  bool moved = false;
+  cudaError_t e;
   explicit Device(int dev) {
-    if (cudaGetDevice(&prev) != cudaSuccess) return;
-    moved = prev != dev;
-    ok = !moved || cudaSetDevice(dev) == cudaSuccess;
+    e = cudaGetDevice(&prev);
+    if (e != cudaSuccess || prev == dev) return;
+    e = cudaSetDevice(dev);
+    moved = true;
   }
   ~Device() {
     if (moved) cudaSetDevice(prev);
   }
 };
-
-int cuda_error(cudaError_t e, const char* what) {
-  return set_error(MSGLA_ERR_CUDA, "%s failed: %s", what, cudaGetErrorString(e));
-}
 
 int esize(int dtype) { return dtype == MSGLA_F32 ? 4 : 2; }
 
@@ -179,7 +183,7 @@ int check_workspace(const NormParams& p, bool backward, void* ws, size_t bytes, 
 
 #define ON_DEVICE(dev)       \
   Device guard(dev);         \
-  if (!guard.ok) return set_error(MSGLA_ERR_CUDA, "cudaSetDevice(%d) failed", dev)
+  if (guard.e != cudaSuccess) return cuda_error(guard.e, "cudaSetDevice")
 
 }  // namespace
 

@@ -91,6 +91,17 @@ cudaError_t allow_shared(int bytes) {
   return e;
 }
 
+// A launch whose own status is returned: cudaGetLastError() after it would also report what another call left.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_plain(void (*kernel)(KArgs...), dim3 grid, dim3 block, int shared, cudaStream_t st, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = shared;
+  cfg.stream = st;
+  return cudaLaunchKernelEx(&cfg, kernel, KArgs(args)...);
+}
+
 // ---------------------------------------------------------------- element types
 enum : int { kBF16 = 0, kF16 = 1, kF32 = 2 };
 enum : int { kActNone = 0, kActSilu = 1, kActSigmoid = 2 };

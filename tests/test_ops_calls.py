@@ -28,3 +28,21 @@ def test_workspace_sizes_are_of_the_named_device():
             assert lib.msgla_group_norm_workspace_size(good, 8, S, gradients, ctypes.byref(n)) == 0
             bad = _lib.NormConfig(torch.cuda.device_count(), 0, 64, 4, 0, 1, 1e-5)
             assert lib.msgla_group_norm_workspace_size(bad, 8, S, gradients, ctypes.byref(n)) < 0
+
+
+def test_a_failed_call_leaves_no_error_behind():
+    """A call for a device that does not exist fails; the good calls after it do not report its error."""
+    lib = _lib.load()
+    x, z, s = randn(2, 64), randn(2, 64, seed=1), randn(2, 64, seed=2)
+    good = [lambda: gated_scan_step(x, z, s), lambda: group_norm(x, 4), lambda: group_norm(x[None], 4),
+            lambda: group_norm_backward(x, group_norm_forward(x, 4)[1]),
+            lambda: group_norm_backward(x[None], group_norm_forward(x[None], 4)[1]), lambda: gated_scan(x[None], z[None])]
+    for f in good:
+        f()
+    rows = lambda t: _lib.Rows(t.data_ptr(), 64, 0)
+    for f in good:
+        bad = _lib.ScanConfig(torch.cuda.device_count(), 2, 64, 0, 16.0)
+        out = torch.empty_like(x)
+        assert lib.msgla_scan_step(bad, 2, rows(x), rows(z), None, s.data_ptr(), rows(out), None) < 0
+        f()
+    torch.cuda.synchronize()
