@@ -45,13 +45,23 @@ def _refuse(message: str, status: int = -1):
 
 
 @functools.lru_cache(maxsize=256)
-def _scan_config(device: int, dtype, D: int, tied, gate_normalizer):
-    return _lib.ScanConfig(device, _DTYPES[dtype], D, 1 if tied else 0, float(gate_normalizer))
+def _scan_config(device: int, dtype, D: int, tied: bool, gate_normalizer: float):
+    return _lib.ScanConfig(device, _DTYPES[dtype], D, 1 if tied else 0, gate_normalizer)
 
 
 @functools.lru_cache(maxsize=256)
 def _norm_config(device: int, dtype, C: int, groups: int, activation, center: bool, eps: float):
     return _lib.NormConfig(device, _DTYPES[dtype], C, groups, _ACTIVATIONS[activation], 1 if center else 0, eps)
+
+
+def _number(name: str, v) -> float:
+    """v as a Python number: the configurations are kept by value, and a tensor's can change."""
+    if type(v) is float:
+        return v
+    try:
+        return float(v)
+    except (TypeError, ValueError, RuntimeError) as e:
+        _refuse(f"{name}={v!r} must be a number ({e})")
 
 
 def _check_x(name: str, t, dims: int):
@@ -175,7 +185,7 @@ def _scan_args(x, gate, mask, gate_normalizer, tied, dims):
         _refuse("x has no channels")
     if mask is not None:
         _check_mask(mask, shape[:-1], x.device)
-    return _scan_config(x.device.index, x.dtype, shape[-1], tied, gate_normalizer), shape
+    return _scan_config(x.device.index, x.dtype, shape[-1], bool(tied), _number("gate_normalizer", gate_normalizer)), shape
 
 
 def _scan_forward(x, gate, mask, initial_state, gate_normalizer, tied, save, out, stream):
@@ -332,7 +342,7 @@ def _norm_forward(x, groups, weight, bias, gate, mask, activation, eps, center, 
     C = x.shape[-1]
     if not isinstance(groups, int) or groups < 1 or C == 0 or C % groups:
         _refuse(f"groups={groups} must be a positive divisor of the {C} channels")
-    if activation not in _ACTIVATIONS:
+    if not (activation is None or isinstance(activation, str)) or activation not in _ACTIVATIONS:
         _refuse(f"activation {activation!r}: none, silu or sigmoid", -2)
     if gate is not None:
         _check_like("gate", gate, x)
@@ -341,7 +351,7 @@ def _norm_forward(x, groups, weight, bias, gate, mask, activation, eps, center, 
             _check_f32(name, t, (C,), x.device)
     if mask is not None:
         _check_mask(mask, x.shape[:-1], x.device)
-    cfg = _norm_config(x.device.index, x.dtype, C, groups, activation, bool(center), float(eps))
+    cfg = _norm_config(x.device.index, x.dtype, C, groups, activation, bool(center), _number("eps", eps))
     N, S = x.shape[0], 1 if x.dim() == 2 else x.shape[1]
     on = _on(x.device, stream, x, weight, bias, gate, mask, out)
     if out is None:

@@ -46,3 +46,33 @@ def test_a_failed_call_leaves_no_error_behind():
         assert lib.msgla_scan_step(bad, 2, rows(x), rows(z), None, s.data_ptr(), rows(out), None) < 0
         f()
     torch.cuda.synchronize()
+
+
+def test_numbers_given_as_tensors_are_read_anew():
+    """gate_normalizer, tied, eps and center as tensors that change between calls."""
+    x, z = randn(2, 40, 16), randn(2, 40, 16, seed=1)
+    tau, tied = torch.tensor(16.0), torch.tensor(False)
+    first = gated_scan(x, z, gate_normalizer=tau, tied=tied)[0]
+    assert torch.equal(first, gated_scan(x, z)[0])
+    tau.fill_(2.0)
+    tied.fill_(True)
+    assert torch.equal(gated_scan(x, z, gate_normalizer=tau, tied=tied)[0], gated_scan(x, z, gate_normalizer=2.0, tied=True)[0])
+    s, t = randn(2, 16), randn(2, 16)
+    gated_scan_step(x[:, 0], z[:, 0], s, gate_normalizer=tau)
+    gated_scan_step(x[:, 0], z[:, 0], t, gate_normalizer=2.0)
+    assert torch.equal(s, t)
+    eps, center = torch.tensor(0.5), torch.tensor(True)
+    group_norm(x, 2, eps=eps, center=center)
+    eps.fill_(2.0)
+    center.fill_(False)
+    assert torch.equal(group_norm(x, 2, eps=eps, center=center), group_norm(x, 2, eps=2.0, center=False))
+
+
+def test_numbers_that_are_none():
+    x = randn(2, 5, 16)
+    for f in (lambda: gated_scan(x, x, gate_normalizer="16s"), lambda: gated_scan(x, x, gate_normalizer=None),
+              lambda: gated_scan(x, x, gate_normalizer=[16.0]), lambda: gated_scan_step(x[:, 0], x[:, 0], x[:, 1].clone(), gate_normalizer=None),
+              lambda: group_norm(x, 4, eps=None), lambda: group_norm(x, 4, eps="x"), lambda: group_norm(x, 4, activation=["silu"]),
+              lambda: group_norm(x, 4.0), lambda: group_norm(x, None)):
+        with pytest.raises(MSGLAError):
+            f()
