@@ -6,7 +6,8 @@ gated_scan        the gated recurrence over sequences, one state per channel:
 gated_scan_step   the same for one token of every sequence, updating the state in place
 group_norm        group normalisation, channels last, with an activation or an output gate
 
-gated_scan and group_norm take part in autograd. The pairs gated_scan_forward /
+gated_scan and group_norm take part in autograd (backwards; forward-mode derivatives are
+refused). The pairs gated_scan_forward /
 gated_scan_backward and group_norm_forward / group_norm_backward do the same by hand:
 the forward returns what its backward needs. Both forms run the kernels of libmsgla.so;
 this module checks arguments, allocates outputs and workspaces, and passes pointers.
@@ -32,6 +33,7 @@ import functools
 from typing import NamedTuple, Optional
 
 import torch
+from torch.autograd import forward_ad
 
 from . import _lib
 from ._lib import MSGLAError
@@ -72,6 +74,15 @@ def _check_x(name: str, t, dims: int):
     if t.dtype not in _DTYPES:
         _refuse(f"{name} has dtype {t.dtype}: bfloat16, float16 or float32", -2)
     _refuse(f"{name} has {t.dim()} dimensions, {dims} are needed")
+
+
+def _refuse_tangents(name: str, *tensors):
+    """Forward-mode derivatives: a dual tensor's tangent would be dropped, which reads as zero."""
+    if getattr(forward_ad, "_current_level", 0) < 0:  # no dual level is open
+        return
+    for t in tensors:
+        if isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None:
+            _refuse(f"{name} has no forward-mode derivatives", -2)
 
 
 def _check_like(name: str, t, x):
@@ -290,6 +301,7 @@ def gated_scan(x, gate, *, mask=None, initial_state=None, gate_normalizer: float
     tied            the input enters as (1 - a_t) x_t instead of x_t.
     out, stream     optional tensor for h, optional stream (neither with gradients).
     """
+    _refuse_tangents("gated_scan", x, gate, initial_state)
     if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in (x, gate, initial_state)):
         if out is not None or stream is not None:
             _refuse("out and stream cannot be combined with gradients: use torch.cuda.stream(..) around both passes")
@@ -308,6 +320,7 @@ def gated_scan_step(x, gate, state, *, mask=None, gate_normalizer: float = 16.0,
     zero. No gradients: use gated_scan for training."""
     cfg, shape = _scan_args(x, gate, mask, gate_normalizer, tied, 2)
     _check_f32("state", state, shape, x.device)
+    _refuse_tangents("gated_scan_step", x, gate, state)
     if torch.is_grad_enabled() and (x.requires_grad or gate.requires_grad or state.requires_grad):
         _refuse("gated_scan_step has no gradients: call it under torch.no_grad()", -2)
     on = _on(x.device, stream, x, gate, mask, state, out)
@@ -437,6 +450,7 @@ def group_norm(x, groups: int, weight=None, bias=None, *, gate=None, mask=None, 
     center          False: divide by the root mean square, without taking the mean off.
     out, stream     optional tensor for y, optional stream (neither with gradients).
     """
+    _refuse_tangents("group_norm", x, weight, bias, gate)
     if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in (x, weight, bias, gate)):
         if out is not None or stream is not None:
             _refuse("out and stream cannot be combined with gradients: use torch.cuda.stream(..) around both passes")

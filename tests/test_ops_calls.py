@@ -48,6 +48,26 @@ def test_a_failed_call_leaves_no_error_behind():
     torch.cuda.synchronize()
 
 
+def test_forward_mode_is_refused():
+    """A dual tensor's tangent would be dropped, and a derivative of zero reported."""
+    import torch.autograd.forward_ad as fwd
+    x, z, s, w = randn(2, 5, 16), randn(2, 5, 16, seed=1), randn(2, 16), torch.ones(16, device="cuda")
+    with fwd.dual_level():
+        dual = lambda t: fwd.make_dual(t, torch.ones_like(t))
+        calls = [lambda: gated_scan(dual(x), z), lambda: gated_scan(x, dual(z)), lambda: gated_scan(x, z, initial_state=dual(s)),
+                 lambda: gated_scan_step(dual(x[:, 0]), z[:, 0], s), lambda: gated_scan_step(x[:, 0], dual(z[:, 0]), s),
+                 lambda: gated_scan_step(x[:, 0], z[:, 0], dual(s)), lambda: group_norm(dual(x), 4),
+                 lambda: group_norm(x, 4, dual(w)), lambda: group_norm(x, 4, w, dual(w)), lambda: group_norm(x, 4, gate=dual(x))]
+        for k, f in enumerate(calls):
+            for grad in (True, False):
+                with torch.set_grad_enabled(grad), pytest.raises(MSGLAError):
+                    f()
+                    pytest.fail(f"call {k} was taken")
+        gated_scan(x, z, initial_state=s)  # without tangents inside a dual level
+        group_norm(x, 4, w, gate=x)
+        gated_scan_step(x[:, 0], z[:, 0], s.clone())
+
+
 def test_numbers_given_as_tensors_are_read_anew():
     """gate_normalizer, tied, eps and center as tensors that change between calls."""
     x, z = randn(2, 40, 16), randn(2, 40, 16, seed=1)
