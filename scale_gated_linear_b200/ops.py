@@ -58,8 +58,6 @@ def _norm_config(device: int, dtype, C: int, groups: int, activation, center: bo
 
 def _number(name: str, v) -> float:
     """v as a Python number: the configurations are kept by value, and a tensor's can change."""
-    if type(v) is float:
-        return v
     try:
         return float(v)
     except (TypeError, ValueError, RuntimeError) as e:
@@ -76,10 +74,13 @@ def _check_x(name: str, t, dims: int):
     _refuse(f"{name} has {t.dim()} dimensions, {dims} are needed")
 
 
+def _dual_level() -> bool:
+    """Whether a level of forward-mode differentiation is open."""
+    return getattr(forward_ad, "_current_level", 0) >= 0
+
+
 def _refuse_tangents(name: str, *tensors):
-    """Forward-mode derivatives: a dual tensor's tangent would be dropped, which reads as zero."""
-    if getattr(forward_ad, "_current_level", 0) < 0:  # no dual level is open
-        return
+    """In a dual level: a dual tensor's tangent would be dropped, which reads as a derivative of zero."""
     for t in tensors:
         if isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None:
             _refuse(f"{name} has no forward-mode derivatives", -2)
@@ -170,6 +171,10 @@ def _on(device, stream, *inputs):
     return _Current(device.index) if stream is None else _On(device, stream, inputs)
 
 
+# A tensor written in place, as autograd's checks of saved tensors know it.
+_written = torch.autograd.graph.increment_version
+
+
 def _check_out(out, x):
     _check_like("out", out, x)
     if out.requires_grad:
@@ -196,7 +201,9 @@ def _scan_args(x, gate, mask, gate_normalizer, tied, dims):
         _refuse("x has no channels")
     if mask is not None:
         _check_mask(mask, shape[:-1], x.device)
-    return _scan_config(x.device.index, x.dtype, shape[-1], bool(tied), _number("gate_normalizer", gate_normalizer)), shape
+    if type(gate_normalizer) is not float:
+        gate_normalizer = _number("gate_normalizer", gate_normalizer)
+    return _scan_config(x.get_device(), x.dtype, shape[-1], True if tied else False, gate_normalizer), shape
 
 
 def _scan_forward(x, gate, mask, initial_state, gate_normalizer, tied, save, out, stream):
@@ -204,7 +211,8 @@ def _scan_forward(x, gate, mask, initial_state, gate_normalizer, tied, save, out
     if initial_state is not None:
         _check_f32("initial_state", initial_state, (B, D), x.device)
     on = _on(x.device, stream, x, gate, mask, initial_state, out)
-    if out is None:
+    own = out is None
+    if own:
         out = on.empty_like(x)
     else:
         _check_out(out, x)
@@ -214,6 +222,8 @@ def _scan_forward(x, gate, mask, initial_state, gate_normalizer, tied, save, out
     _lib.check(_lib.load().msgla_scan_forward(cfg, B, L, _rows3("x", x), _rows3("gate", gate), _ptr(mask),
                                               _ptr(initial_state), _rows3("out", out), last.data_ptr(), _ptr(states),
                                               on.handle))
+    if not own:
+        _written(out)
     saved = ScanSaved(x, gate, mask, states, cfg, initial_state is not None) if save else None
     return out, last, saved
 
@@ -301,7 +311,8 @@ def gated_scan(x, gate, *, mask=None, initial_state=None, gate_normalizer: float
     tied            the input enters as (1 - a_t) x_t instead of x_t.
     out, stream     optional tensor for h, optional stream (neither with gradients).
     """
-    _refuse_tangents("gated_scan", x, gate, initial_state)
+    if _dual_level():
+        _refuse_tangents("gated_scan", x, gate, initial_state)
     if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in (x, gate, initial_state)):
         if out is not None or stream is not None:
             _refuse("out and stream cannot be combined with gradients: use torch.cuda.stream(..) around both passes")
@@ -320,16 +331,22 @@ def gated_scan_step(x, gate, state, *, mask=None, gate_normalizer: float = 16.0,
     zero. No gradients: use gated_scan for training."""
     cfg, shape = _scan_args(x, gate, mask, gate_normalizer, tied, 2)
     _check_f32("state", state, shape, x.device)
-    _refuse_tangents("gated_scan_step", x, gate, state)
+    if _dual_level():
+        _refuse_tangents("gated_scan_step", x, gate, state)
     if torch.is_grad_enabled() and (x.requires_grad or gate.requires_grad or state.requires_grad):
         _refuse("gated_scan_step has no gradients: call it under torch.no_grad()", -2)
-    on = _on(x.device, stream, x, gate, mask, state, out)
-    if out is None:
+    on = _Current(x.get_device()) if stream is None else _On(x.device, stream, (x, gate, mask, state, out))
+    own = out is None
+    if own:
         out = on.empty_like(x)
     else:
         _check_out(out, x)
-    _lib.check(_lib.load().msgla_scan_step(cfg, shape[0], _rows2("x", x), _rows2("gate", gate), _ptr(mask), state.data_ptr(),
-                                           _rows2("out", out), on.handle))
+    status = _lib.load().msgla_scan_step(cfg, shape[0], _rows2("x", x), _rows2("gate", gate),
+                                         None if mask is None else mask.data_ptr(), state.data_ptr(), _rows2("out", out),
+                                         on.handle)
+    if status:
+        _lib.check(status)
+    _written(state if own else (state, out))
     return out
 
 
@@ -367,7 +384,8 @@ def _norm_forward(x, groups, weight, bias, gate, mask, activation, eps, center, 
     cfg = _norm_config(x.device.index, x.dtype, C, groups, activation, bool(center), _number("eps", eps))
     N, S = x.shape[0], 1 if x.dim() == 2 else x.shape[1]
     on = _on(x.device, stream, x, weight, bias, gate, mask, out)
-    if out is None:
+    own = out is None
+    if own:
         out = on.empty_like(x)
     else:
         _check_out(out, x)
@@ -376,6 +394,8 @@ def _norm_forward(x, groups, weight, bias, gate, mask, activation, eps, center, 
     _lib.check(_lib.load().msgla_group_norm_forward(
         cfg, N, S, _rows("x", x), None if gate is None else _rows("gate", gate), _ptr(weight), _ptr(bias), _ptr(mask),
         _rows("out", out), _ptr(stats), _ptr(ws), nbytes, on.handle))
+    if not own:
+        _written(out)
     return out, (NormSaved(x, gate, weight, bias, mask, stats, cfg) if save else None)
 
 
@@ -450,7 +470,8 @@ def group_norm(x, groups: int, weight=None, bias=None, *, gate=None, mask=None, 
     center          False: divide by the root mean square, without taking the mean off.
     out, stream     optional tensor for y, optional stream (neither with gradients).
     """
-    _refuse_tangents("group_norm", x, weight, bias, gate)
+    if _dual_level():
+        _refuse_tangents("group_norm", x, weight, bias, gate)
     if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in (x, weight, bias, gate)):
         if out is not None or stream is not None:
             _refuse("out and stream cannot be combined with gradients: use torch.cuda.stream(..) around both passes")

@@ -96,3 +96,60 @@ def test_numbers_that_are_none():
               lambda: group_norm(x, 4.0), lambda: group_norm(x, None)):
         with pytest.raises(MSGLAError):
             f()
+
+
+def test_updates_in_place_are_seen_by_autograd():
+    """A state (or an output buffer) that a living graph has saved: its backward reports the change,
+    as after torch's own in-place operations, in place of a wrong gradient."""
+    x, z, state = randn(2, 16), randn(2, 16, seed=1), randn(2, 16, seed=2)
+    w = torch.ones(16, device="cuda", requires_grad=True)
+    seq = randn(2, 3, 16)
+
+    def changed(t, call):
+        y = (t * w).sum()
+        with torch.no_grad():
+            call()
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.backward()
+
+    changed(state, lambda: gated_scan_step(x, z, state))
+    h = torch.zeros_like(x)
+    changed(h, lambda: gated_scan_step(x, z, state, out=h))
+    hs = torch.zeros_like(seq)
+    changed(hs, lambda: gated_scan(seq, seq, out=hs))
+    changed(hs, lambda: group_norm(seq, 4, out=hs))
+    changed(hs, lambda: gated_scan_forward(seq, seq, out=hs))
+    changed(hs, lambda: group_norm_forward(seq, 4, out=hs))
+    with torch.inference_mode():  # tensors without a version counter
+        s = state.clone()
+        gated_scan_step(x, z, s, out=torch.empty_like(x))
+    gated_scan_step(x, z, s)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_captured_steps(dtype):
+    """Tokens through the step and a head norm in one replayed graph: what the eager calls give."""
+    B, D, heads = 5, 96, 4
+    xs, zs, gs = (randn(6, B, D, dtype=dtype, seed=k) for k in range(3))
+    w = randn(D)
+    x, z, g, mask = xs[0].clone(), zs[0].clone(), gs[0].clone(), torch.ones(B, dtype=torch.uint8, device="cuda")
+    state = randn(B, D, seed=9)
+
+    def token(x, z, g, state, mask):
+        return group_norm(gated_scan_step(x, z, state, mask=mask, tied=True), heads, w, gate=g, activation="silu")
+
+    with torch.no_grad():
+        token(x, z, g, state.clone(), mask)
+        torch.cuda.synchronize()
+        kept = state.clone()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            y = token(x, z, g, state, mask)
+        want = kept.clone()
+        for k in range(6):
+            for a, b in ((x, xs[k]), (z, zs[k]), (g, gs[k])):
+                a.copy_(b)
+            mask.copy_((torch.arange(B) % 3 != k % 3).to(torch.uint8))
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(y, token(xs[k], zs[k], gs[k], want, mask)) and torch.equal(state, want)
