@@ -22,9 +22,11 @@ these rules raises MSGLAError before anything is launched.
 Capturing a backward pass into a CUDA graph: autograd adds a leaf's gradient on the stream
 that was current when the leaf first joined a graph that still lives. If that is an eager
 graph of the same leaf, the capture would break inside the autograd engine, so gated_scan
-and group_norm refuse a captured call then (and one whose leaf another operation of the same
-capture has used before them, which looks the same). Drop the eager outputs first, or capture
-the explicit pairs, which keep autograd out.
+and group_norm refuse a captured call then. torch does not tell the stream of a node, so a
+captured call is refused for every leaf whose node lives and was not first used by these
+functions in that capture: a leaf that another operation of the same capture has used before
+them, and a leaf whose node something holds for its whole life, as data-parallel wrappers do.
+Drop the eager outputs first, or capture the explicit pairs, which keep autograd out.
 """
 from __future__ import annotations
 
@@ -54,6 +56,14 @@ def _scan_config(device: int, dtype, D: int, tied: bool, gate_normalizer: float)
 @functools.lru_cache(maxsize=256)
 def _norm_config(device: int, dtype, C: int, groups: int, activation, center: bool, eps: float):
     return _lib.NormConfig(device, _DTYPES[dtype], C, groups, _ACTIVATIONS[activation], 1 if center else 0, eps)
+
+
+@functools.lru_cache(maxsize=8)
+def _saved_rows(dtype) -> int:
+    """Rows between two states that a forward saves, as the library keeps them."""
+    n, L = ctypes.c_size_t(), 1 << 16
+    _lib.check(_lib.load().msgla_scan_saved_size(_lib.ScanConfig(0, _DTYPES[dtype], 1, 0, 1.0), 1, L, ctypes.byref(n)))
+    return 4 * L // n.value
 
 
 def _number(name: str, v) -> float:
@@ -217,8 +227,7 @@ def _scan_forward(x, gate, mask, initial_state, gate_normalizer, tied, save, out
     else:
         _check_out(out, x)
     last = on.empty((B, D), torch.float32, x.device)
-    rows = 8 if x.dtype == torch.float32 else 16
-    states = on.empty((B, (L + rows - 1) // rows, D), torch.float32, x.device) if save else None
+    states = on.empty((B, -(-L // _saved_rows(x.dtype)), D), torch.float32, x.device) if save else None
     _lib.check(_lib.load().msgla_scan_forward(cfg, B, L, _rows3("x", x), _rows3("gate", gate), _ptr(mask),
                                               _ptr(initial_state), _rows3("out", out), last.data_ptr(), _ptr(states),
                                               on.handle))

@@ -153,3 +153,13 @@ def test_captured_steps(dtype):
             graph.replay()
             torch.cuda.synchronize()
             assert torch.equal(y, token(xs[k], zs[k], gs[k], want, mask)) and torch.equal(state, want)
+
+
+def test_saved_states_have_the_librarys_size():
+    lib, n = _lib.load(), ctypes.c_size_t()
+    for code, dtype in ((0, BF16), (1, torch.float16), (2, F32)):
+        for L in (1, 7, 8, 9, 16, 17, 100):
+            x = randn(2, L, 24, dtype=dtype)
+            states = gated_scan_forward(x, x)[2].states
+            assert lib.msgla_scan_saved_size(_lib.ScanConfig(0, code, 24, 0, 16.0), 2, L, ctypes.byref(n)) == 0
+            assert states.numel() * 4 == n.value
