@@ -163,3 +163,24 @@ def test_saved_states_have_the_librarys_size():
             states = gated_scan_forward(x, x)[2].states
             assert lib.msgla_scan_saved_size(_lib.ScanConfig(0, code, 24, 0, 16.0), 2, L, ctypes.byref(n)) == 0
             assert states.numel() * 4 == n.value
+
+
+def test_a_captured_call_refuses_a_leaf_whose_node_is_held():
+    """A wrapper that keeps a leaf's gradient node: torch does not tell the node's stream. The explicit
+    pair is what such a program captures."""
+    w, x = torch.ones(16, device="cuda", requires_grad=True), randn(4, 16)
+    held = torch.autograd.graph.get_gradient_edge(w).node
+    group_norm(x, 4, w)
+    torch.cuda.synchronize()
+    with pytest.raises(MSGLAError, match="explicit"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            group_norm(x, 4, w)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y, saved = group_norm_forward(x, 4, w.detach())
+        grads = group_norm_backward(x, saved)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, group_norm(x, 4, w.detach())) and grads[1].shape == w.shape
+    del held
