@@ -899,7 +899,7 @@ struct HoldPlan {
   int tiles, groups;      // tiles, groups a tile
   int shared;             // bytes
 };
-constexpr int kMaxHold = 8, kMaxHoldGroups = 32;
+constexpr int kMaxHold = 8;
 constexpr int kHoldShared = 212 * 1024;  // most that a block asks for
 
 template <typename T, int V, int TENSORS>
@@ -1224,7 +1224,6 @@ bool hold_plan(const NormParams& p, int v, int tensors, HoldPlan& q) {
   q.groups = q.width / cg;
   q.tx = q.width / v;
   q.ty = kThreads / q.tx;
-  if (q.groups > kMaxHoldGroups || q.ty < 1) return false;
   if (q.ty > p.S) q.ty = static_cast<int>(p.S);
   q.tiles = (p.C + q.width - 1) / q.width;
   const long long bytes = p.S * q.tx * 16 * tensors, units = p.N * q.tiles;

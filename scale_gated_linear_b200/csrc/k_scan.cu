@@ -521,7 +521,7 @@ __device__ __forceinline__ void fetch(uint8_t* to, const Lane<T, VEC>& l, bool f
       }
     }
   } else {
-using Raw = typename Pair<T>::Raw;
+    using Raw = typename Pair<T>::Raw;
     Raw* at = reinterpret_cast<Raw*>(to) + lane;
     constexpr int kStep = Lane<T, VEC>::kRow / sizeof(Raw);
     if (sizeof(T) == 4) {
@@ -697,7 +697,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) scan_forward_kernel(const __gr
   constexpr int R = kRowsOf<T>, kRows = kWarps * R;
   extern __shared__ __align__(128) uint8_t dynamic[];
   __shared__ Join warps[2][kWarps][32];
-  const int cluster = p.cluster, rank = cluster > 1 ? cluster_ctarank() : 0;
+  const int cluster = p.cluster, rank = cluster_ctarank();
   const int w = warp_id(), lane = lane_id(), b = blockIdx.y;
   const int c0 = blockIdx.x / cluster * 64, ch = c0 + 2 * lane, n = min(max(p.D - ch, 0), 2);
   uint8_t* mine = dynamic + w * 3 * 2 * kRowsBytes;
@@ -739,7 +739,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) scan_forward_kernel(const __gr
 
   uint32_t now = start_step(0), next = start_step(1);
   uint64_t carry = p.h0 ? load_state<VEC>(p.h0 + state_at, n) : 0ull;
-  if (cluster > 1) cluster_sync();  // every block runs before another writes to it
+  cluster_sync();  // every block runs before another writes to it
   uint64_t nc[R], nc_next[R];
   local(0, nc);
   for (int step = 0; step < steps; ++step) {
@@ -748,16 +748,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) scan_forward_kernel(const __gr
     Join before, all;
     join_warps<kWarps>(warps[step & 1], w, before, all);
     Join* slots = reinterpret_cast<Join*>(dynamic + kForwardRows) + (step & 1) * cluster * 32;
-    if (cluster > 1) send_join(slots, rank, cluster, all, w == 0);
+    send_join(slots, rank, cluster, all, w == 0);
     const uint32_t after = start_step(step + 2);
     if (step + 1 < steps) local(step + 1, nc_next);
-    uint64_t h = carry;
-    if (cluster > 1) {
-      receive_joins();
-      h = pass_blocks(slots, rank, cluster, carry);
-    } else {
-      carry = f2_fma(all.p, carry, all.v);
-    }
+    receive_joins();
+    uint64_t h = pass_blocks(slots, rank, cluster, carry);
     h = f2_fma(before.p, h, before.v);
     if (p.saved && t0 < p.L) store_state<VEC>(p.saved + (static_cast<size_t>(b) * chunks + t0 / R) * p.D + ch, n, h);
     Raw* xs = rows_of(step);
@@ -1022,7 +1017,7 @@ __global__ void __launch_bounds__(kBackWarps * 32, 1) scan_backward_kernel(const
   extern __shared__ __align__(128) uint8_t dynamic[];
   __shared__ Join warps[2][kBackWarps][32];
   __shared__ uint32_t last_bad[32];  // lanes' channels whose last state is not finite
-  const int cluster = p.cluster, rank = cluster > 1 ? cluster_ctarank() : 0;
+  const int cluster = p.cluster, rank = cluster_ctarank();
   const int w = warp_id(), lane = lane_id(), b = blockIdx.y;
   const int c0 = blockIdx.x / cluster * 64, ch = c0 + 2 * lane, n = min(max(p.D - ch, 0), 2);
   uint8_t* mine = dynamic + w * 3 * 3 * kRowsBytes;
@@ -1075,7 +1070,7 @@ __global__ void __launch_bounds__(kBackWarps * 32, 1) scan_backward_kernel(const
 
   Step now = start_step(0), next = start_step(1);
   uint64_t carry = p.dlast ? load_state<VEC>(p.dlast + state_at, n) : 0ull;
-  if (cluster > 1) cluster_sync();
+  cluster_sync();
   uint64_t nc[R], nc_next[R];
   const uint32_t state_bad = not_finite(local(0, now.state, nc), n);
   if (rank == 0 && w == 0)  // it has the sequence's last state; sent to the blocks with the first step's joins
@@ -1086,16 +1081,11 @@ __global__ void __launch_bounds__(kBackWarps * 32, 1) scan_backward_kernel(const
     Join before, all;
     join_warps<kBackWarps>(warps[step & 1], w, before, all);
     Join* slots = reinterpret_cast<Join*>(dynamic + kBackRows) + (step & 1) * cluster * 32;
-    if (cluster > 1) send_join(slots, rank, cluster, all, w == 0);
+    send_join(slots, rank, cluster, all, w == 0);
     const Step after = start_step(step + 2);
     if (step + 1 < steps) local(step + 1, next.state, nc_next);
-    uint64_t in = carry;
-    if (cluster > 1) {
-      receive_joins();
-      in = pass_blocks(slots, rank, cluster, carry);
-    } else {
-      carry = f2_fma(all.p, carry, all.v);
-    }
+    receive_joins();
+    uint64_t in = pass_blocks(slots, rank, cluster, carry);
     in = f2_fma(before.p, in, before.v);
     Raw* xs = rows_of(step);
     Raw* zs = xs + kTensor;
@@ -1173,9 +1163,9 @@ bool aligned_rows(const Rows& r, int run, int dtype) {
 }
 bool aligned_state(const float* s) { return reinterpret_cast<uintptr_t>(s) % 8 == 0; }
 
-// Clusters of 1 .. kMaxCluster blocks of a split-rows kernel that run at once on the current device
-// (its blocks fill an SM, and a cluster stays inside one of the GPU's SM groups: on a B200 148,
-// 74, .. 33 of 4, .. 15 of 8), asked for once a device.
+// Clusters of 2 .. kMaxCluster blocks of a split-rows kernel that run at once on the current device
+// (its blocks fill an SM, and a cluster stays inside one of the GPU's SM groups: on a B200 74,
+// .. 33 of 4, .. 15 of 8), asked for once a device.
 template <int KIND>  // 0: forward, 1: backward
 const int* clusters_at_once(const void* kernel, int threads, int shared) {
   constexpr int kDevices = 64;
@@ -1184,7 +1174,7 @@ const int* clusters_at_once(const void* kernel, int threads, int shared) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) dev = 0;
   std::call_once(once[dev], [&] {
-    for (int c = 1; c <= kMaxCluster; ++c) {
+    for (int c = 2; c <= kMaxCluster; ++c) {
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3(c);
       cfg.blockDim = dim3(threads);
@@ -1213,13 +1203,13 @@ const int* clusters_at_once(const void* kernel, int threads, int shared) {
 // against 519), unless the rows are few (256 rows: 5.8 us against 5.3, 1024: 7.4 against 12.7).
 bool one_block(long long tiles, int L, int rows, int pairs) { return tiles > pairs || L <= 2 * rows; }
 
-// Blocks of a cluster: the fewest waves times steps, and of those the fewest blocks.
+// Blocks of a cluster, two at least: the fewest waves times steps, and of those the fewest blocks.
 int pick_cluster(long long tiles, int L, int rows, const int* at_once) {
-  int best = 1;
+  int best = 2;
   long long least = 0;
-  for (int c = 1; c <= kMaxCluster; ++c) {
+  for (int c = 2; c <= kMaxCluster; ++c) {
     const long long time = (tiles + at_once[c] - 1) / at_once[c] * ((L + static_cast<long long>(c) * rows - 1) / (static_cast<long long>(c) * rows));
-    if (c == 1 || time < least) best = c, least = time;
+    if (c == 2 || time < least) best = c, least = time;
   }
   return best;
 }
