@@ -57,6 +57,27 @@ def test_held_near_the_limit(N, S, C, G, dtype, gated, center):
     compare(x, G, 1 + 0.3 * r(C), 0.3 * r(C), gate, mask, "silu", center, dy, 1e-5, HELD, dtype)
 
 
+# A group of more than 256 vectors, a tile of more than 1.6 MB, and groups that tile borders cut
+@pytest.mark.parametrize("mask", [None, "random", "empty"])
+@pytest.mark.parametrize("N,S,C,G,dtype", [(2, 300, 4096, 1, BF16), (3, 300, 2048, 1, F32), (2, 14000, 64, 1, BF16),
+                                           (1, 7001, 64, 2, F32), (2, 65, 6600, 3, F16)])
+def test_two_passes(N, S, C, G, dtype, mask):
+    for gated, center in ((True, False), (False, True)):
+        check(N, S, C, G, dtype, act="silu", gated=gated, mask=mask, center=center, seed=S, eps=1e-3)
+
+
+@pytest.mark.parametrize("N,S,C,G,dtype", [(2, 300, 4096, 1, BF16), (1, 14000, 64, 1, BF16), (1, 7001, 64, 2, F32), (2, 1030, 32, 1, F32)])
+def test_forms_agree(N, S, C, G, dtype):
+    """The same rows from an odd start, which are taken one element at a time: within both forms' bounds."""
+    from scale_gated_linear_b200 import group_norm
+    g = torch.Generator().manual_seed(S)
+    x = (torch.randn(N, S, C, generator=g) + 3).to(dtype)
+    odd = torch.empty(x.numel() + 1, dtype=dtype, device="cuda")[1:].view(x.shape).copy_(x)
+    a, b = group_norm(x.cuda(), G, activation="silu"), group_norm(odd, G, activation="silu")
+    ey = oo.norm_error(host(x), G, act="silu")
+    near(a, host(b), 2 * HELD * ey + (0 if dtype == F32 else 2.0 ** -8) * np.abs(host(b)), dtype)
+
+
 @pytest.mark.parametrize("center", [True, False])
 @pytest.mark.parametrize("N,S,C,G", [(2, 4096, 64, 1), (1, 16384, 8, 1), (1, 1000, 256, 8), (2, 14000, 64, 1), (2, 300, 2048, 1)])
 def test_constant_samples(N, S, C, G, center):
