@@ -1018,8 +1018,8 @@ __global__ void __launch_bounds__(kThreads, 4) norm_hold_forward_kernel(const No
         for (int e = 0; e < V; ++e) sum += f[e];
       }
   const float2 total = h.group_sum(make_float2(sum, 0.f), h.valid_rows(), 0, cg, count);
-  const float elements = fmaxf(count * cg, 1.f);
-  float mean = p.center ? total.x / elements : 0.f;
+  const float share = 1.f / fmaxf(count * cg, 1.f);
+  float mean = p.center ? total.x * share : 0.f;
   const uint64_t minus = f2_pack(-mean, -mean);
   uint64_t off = 0, squares = 0;
   if (h.here)
@@ -1037,9 +1037,9 @@ __global__ void __launch_bounds__(kThreads, 4) norm_hold_forward_kernel(const No
   // the sum of up to 400 values a thread left the mean off by a few of its steps, which the differences show
   const float2 o = f2_unpack(off), sq = f2_unpack(squares);
   float2 about = h.group_sum(make_float2(o.x + o.y, sq.x + sq.y), 0.f, 1, cg, count);
-  about.x = p.center ? about.x / elements : 0.f;
+  about.x = p.center ? about.x * share : 0.f;
   mean += about.x;
-  const float rstd = 1.f / sqrtf(fmaxf(about.y / elements - about.x * about.x, 0.f) + p.eps);
+  const float rstd = 1.f / sqrtf(fmaxf(fmaf(-about.x, about.x, about.y * share), 0.f) + p.eps);
   if (!h.here) return;
   if (p.stats && h.rank == 0 && h.ty == 0 && h.c % cg == 0)
     *reinterpret_cast<float2*>(p.stats + 2 * (h.n * p.G + h.c / cg)) = make_float2(mean, rstd);
