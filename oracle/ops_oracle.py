@@ -165,7 +165,9 @@ def group_norm(x, groups, w=None, b=None, gate=None, mask=None, act="none", eps=
 def norm_error(x, groups, w=None, b=None, gate=None, mask=None, act="none", eps=1e-5, center=True, dy=None):
     """Bounds of the f32 error of y, and with dy of (dx, dw, db, dgate). K counts roundings: a
     sum takes at most 96 additions in a row in one thread and fewer than 32 joins after
-    it, a value passes fewer than 64 other roundings (sigmoid's 8, products, differences)."""
+    it, a value passes fewer than 64 other roundings (sigmoid's 8, products, differences). The
+    squares of samples held in shared memory take up to 200 additions in a row, of which the
+    root of the variance hands on half; their mean is corrected by a second sum."""
     K = 192 * U
     N, S, C = x.shape
     cg = C // groups

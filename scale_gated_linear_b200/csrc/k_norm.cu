@@ -22,7 +22,8 @@
 // 78 us forward and backward held in shared memory, 97 in two passes.
 // Variances are sums of squared differences: from the mean itself in registers; held, from a mean that
 // the sum of the differences corrects; in two passes from each thread's first value, joined by count, mean and
-// sum of squares. So a mean far from zero costs no digits. Everything is summed in f32 in a fixed order.
+// sum of squares. So a mean far from zero costs what rounding it to f32 costs (in registers, the few additions
+// of a row's team too). Everything is summed in f32 in a fixed order.
 #include <type_traits>
 
 #include "ops_internal.h"

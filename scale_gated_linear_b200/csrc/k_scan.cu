@@ -16,7 +16,7 @@
 // out); the forward states that the backward needs are rebuilt from one saved f32 state a chunk
 // of 16 rows (8 of f32; an eighth of a tensor's bytes), which costs less than reading h would
 // and keeps them in 32 bits. Next to it the issue rate: at HBM's rate the SMs have 33 (forward)
-// and 55 (backward) issue slots an element, and spend 26 and 42. So the gate runs on packed
+// and 55 (backward) issue slots an element, and spend 27 and 42. So the gate runs on packed
 // f32x2 polynomials with one ex2 an element, accurate in c and not only in a: the hardware's
 // log2 alone is off by 2^-22 of one, which is all of c for a gate near one.
 //
