@@ -176,3 +176,18 @@ def test_step_of_infinite_states(tau, dtype):
             want, last, _ = oo.scan(host(x), host(z), tau, tied, M.numpy()[:, None], host(h0))
         same_values(h, want[:, 0], dtype)
         same_values(state, last, F32)
+
+
+@pytest.mark.parametrize("B,L,D", FORMS)
+def test_infinite_values_without_output_gradients(B, L, D):
+    """No gradient of h, an infinite state and an infinite gradient of the last one."""
+    from scale_gated_linear_b200 import gated_scan_backward, gated_scan_forward
+    x, z, _, h0, _, dlast = inputs(B, L, D, F32, bias=1.0, state=True, seed=6)
+    h0[0, 2], dlast[0, 4] = float("inf"), float("-inf")
+    for tied in (False, True):
+        saved = gated_scan_forward(x.cuda(), z.cuda(), initial_state=h0.cuda(), tied=tied)[2]
+        got = gated_scan_backward(None, dlast.cuda(), saved)
+        with np.errstate(invalid="ignore"):
+            want = oo.scan_backward(None, host(dlast), host(x), host(z), 16.0, tied, None, host(h0))[:3]
+        for a, w in zip(got, want):
+            same_values(a, w, F32)
