@@ -517,11 +517,12 @@ __global__ void __launch_bounds__(1024) norm_weights_kernel(const NormParams p, 
 
 // ---------------------------------------------------------------- blocks of rows and channels
 // Block (n, chunk, tile): `ty` rows at a time of tx vectors of channels. Workspace: per (n,
-// chunk) and segment (the part of a group inside a tile) two numbers at the segment's first
-// channel; with gradients also per channel.
+// chunk) and segment (the part of group g inside tile t, number g + t of at most groups + tiles)
+// two numbers; with gradients also per channel.
 struct BlockPlan {
   int tx, ty, width;  // threads along channels and rows, channels a tile
   int tiles, chunks, rows;  // rows a chunk
+  int segments;             // groups + tiles
 };
 
 struct Part {
@@ -547,7 +548,7 @@ __device__ __forceinline__ uint32_t rows_valid(const uint8_t* m, long long s, lo
 }
 
 // Forward sums: float2 (mean, sum of squared differences) per segment at
-// seg[(n * chunks + chunk) * C + channel]; the valid rows of each (n, chunk) at rows_of.
+// seg[(n * chunks + chunk) * segments + segment]; the valid rows of each (n, chunk) at rows_of.
 template <typename T, int V>
 __global__ void __launch_bounds__(kThreads) norm_sums_kernel(const NormParams p, const BlockPlan q, float2* seg, float* rows_of) {
   __shared__ float2 cell[kThreads];  // a thread's V channels: mean and squares
@@ -628,7 +629,7 @@ __global__ void __launch_bounds__(kThreads) norm_sums_kernel(const NormParams p,
       sqs += v.y + counts[r] * V * d * d;
     }
     sqs = team_sum(sqs, 32);
-    if (lane_id() == 0) seg[(part.n * q.chunks + part.chunk) * p.C + a] = make_float2(mean, sqs);
+    if (lane_id() == 0) seg[(part.n * q.chunks + part.chunk) * q.segments + g + part.tile] = make_float2(mean, sqs);
   }
 }
 
@@ -650,7 +651,7 @@ __device__ __forceinline__ float2 join_stats(const NormParams& p, const BlockPla
   Moments m{0.f, 0.f, 0.f};
   for (int i = lane_id(); i < segs * q.chunks; i += 32) {
     const int chunk = i / segs, t = t0 + i % segs, lo = max(a, t * q.width), hi = min(a + cg, (t + 1) * q.width);
-    const float2 v = seg[(n * q.chunks + chunk) * p.C + lo];
+    const float2 v = seg[(n * q.chunks + chunk) * q.segments + g + t];
     m.join(rows_of[n * q.chunks + chunk] * (hi - lo), v.x, v.y);
   }
 #pragma unroll
@@ -809,7 +810,7 @@ __global__ void __launch_bounds__(kThreads, 2) norm_grad_sums_kernel(const NormP
     }
     s1v = team_sum(s1v, 32);
     s2v = team_sum(s2v, 32);
-    if (lane_id() == 0) seg[at_part * p.C + a] = make_float2(s1v, s2v);
+    if (lane_id() == 0) seg[at_part * q.segments + g + part.tile] = make_float2(s1v, s2v);
   }
 }
 
@@ -827,7 +828,7 @@ __global__ void __launch_bounds__(kThreads, 2) norm_grad_apply_kernel(const Norm
     float s1v = 0.f, s2v = 0.f, count = 0.f;
     for (int i = lane_id(); i < segs * q.chunks; i += 32) {
       const size_t row = static_cast<size_t>(part.n) * q.chunks + i / segs;
-      const float2 v = seg[row * p.C + max(a, (first + i % segs) * q.width)];
+      const float2 v = seg[row * q.segments + g + first + i % segs];
       s1v += v.x;
       s2v += v.y;
       if (i % segs == 0) count += rows_of[row];
@@ -1209,6 +1210,7 @@ BlockPlan block_plan(const NormParams& p, int v, int per_sm) {
   if (chunks > most) chunks = most;
   q.rows = static_cast<int>((rows_at_once + chunks - 1) / chunks) * q.ty;
   q.chunks = static_cast<int>((p.S + q.rows - 1) / q.rows);
+  q.segments = p.G + q.tiles;
   return q;
 }
 
@@ -1256,7 +1258,7 @@ struct BlockSpace {
     const size_t parts = static_cast<size_t>(p.N) * q.chunks;
     uint8_t* at = static_cast<uint8_t*>(p.workspace);
     seg = reinterpret_cast<float2*>(at);
-    const size_t a = round256(parts * p.C * 8), b = round256(parts * 4);
+    const size_t a = round256(parts * q.segments * 8), b = round256(parts * 4);
     rows_of = reinterpret_cast<float*>(at + a);
     chan = reinterpret_cast<float*>(at + a + b);
     bytes = a + b + (backward ? round256(parts * p.C * 8) : 0);

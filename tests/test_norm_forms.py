@@ -103,3 +103,16 @@ def test_far_mean(N, S, C, G):
     want = oo.group_norm(host(x), G)
     err = 2.0 ** -24 * (24 * 301 + 3 * 192 * (1 + np.abs(want)))
     near(group_norm(x.cuda(), G), want, err, F32)
+
+
+def test_workspace_of_many_short_samples():
+    """A forward keeps two numbers a group and tile, a backward two a channel beside them: below the tensors' own bytes
+    forward, twice the f32 bytes of a row a sample backward."""
+    import ctypes
+    from scale_gated_linear_b200 import _lib
+    lib, n = _lib.load(), ctypes.c_size_t()
+    N, S, C = 1000000, 2, 64
+    for G in (1, 4):
+        cfg = _lib.NormConfig(0, 0, C, G, 0, 1, 1e-5)
+        assert lib.msgla_group_norm_workspace_size(cfg, N, S, 0, ctypes.byref(n)) == 0 and n.value <= N * (8 * (G + 4) + 4) + 1024
+        assert lib.msgla_group_norm_workspace_size(cfg, N, S, 1, ctypes.byref(n)) == 0 and n.value <= N * (8 * (G + 4) + 4 + 8 * C) + 1024
