@@ -1041,7 +1041,9 @@ __global__ void __launch_bounds__(kThreads, 4) norm_hold_forward_kernel(const No
   float2 about = h.group_sum(make_float2(o.x + o.y, sq.x + sq.y), 0.f, 1, cg, count);
   about.x = p.center ? about.x * share : 0.f;
   mean += about.x;
-  const float rstd = 1.f / sqrtf(fmaxf(fmaf(-about.x, about.x, about.y * share), 0.f) + p.eps);
+  float var = fmaf(-about.x, about.x, about.y * share);
+  if (var < 0.f) var = 0.f;  // and not fmaxf(), which would make 0 of a NaN
+  const float rstd = 1.f / sqrtf(var + p.eps);
   if (!h.here) return;
   if (p.stats && h.rank == 0 && h.ty == 0 && h.c % cg == 0)
     *reinterpret_cast<float2*>(p.stats + 2 * (h.n * p.G + h.c / cg)) = make_float2(mean, rstd);

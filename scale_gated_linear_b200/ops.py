@@ -70,7 +70,7 @@ def _number(name: str, v) -> float:
     """v as a Python number: the configurations are kept by value, and a tensor's can change."""
     try:
         return float(v)
-    except (TypeError, ValueError, RuntimeError) as e:
+    except (TypeError, ValueError, OverflowError, RuntimeError) as e:
         _refuse(f"{name}={v!r} must be a number ({e})")
 
 

@@ -116,3 +116,33 @@ def test_workspace_of_many_short_samples():
         cfg = _lib.NormConfig(0, 0, C, G, 0, 1, 1e-5)
         assert lib.msgla_group_norm_workspace_size(cfg, N, S, 0, ctypes.byref(n)) == 0 and n.value <= N * (8 * (G + 4) + 4) + 1024
         assert lib.msgla_group_norm_workspace_size(cfg, N, S, 1, ctypes.byref(n)) == 0 and n.value <= N * (8 * (G + 4) + 4 + 8 * C) + 1024
+
+
+@pytest.mark.parametrize("center", [True, False])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("shape,G", [((6, 96), 3), ((3, 9000), 2), ((2, 40, 64), 4), ((1, 2000, 40), 5), ((2, 300, 4096), 2), ((2, 21, 33), 3)])
+def test_values_that_are_not_finite(shape, G, dtype, center):
+    """A NaN makes its group NaN, in y and in the gradients; an infinity too where the mean is taken off, and else
+    leaves x / inf: the weight-less finite values at the bias. Other groups keep their bits."""
+    from scale_gated_linear_b200 import group_norm, group_norm_backward, group_norm_forward
+    g = torch.Generator().manual_seed(1)
+    x, dy = torch.randn(*shape, generator=g).to(dtype).cuda(), torch.randn(*shape, generator=g).to(dtype).cuda()
+    cg = shape[-1] // G
+    b = torch.randn(shape[-1], generator=g).cuda()
+    clean = group_norm(x, G, None, b, center=center)
+    hit = torch.zeros(shape, dtype=torch.bool, device="cuda")
+    hit[-1, ..., cg:2 * cg] = True
+    at = (-1, cg + 1) if len(shape) == 2 else (-1, shape[1] // 2, cg + 1)
+    for bad in (float("nan"), float("inf")):
+        x2 = x.clone()
+        x2[at] = bad
+        y, saved = group_norm_forward(x2, G, None, b, center=center)
+        assert torch.equal(y[~hit], clean[~hit])
+        if bad != bad or center:
+            assert torch.isnan(y[hit]).all()
+            dx, _, db, _ = group_norm_backward(dy, saved)
+            assert torch.isnan(dx[hit]).all() and not torch.isnan(dx[~hit]).any()
+        else:
+            want = b.to(dtype).expand(shape).clone()
+            want[at] = bad - bad
+            assert torch.equal(y[hit].nan_to_num(7.0), want[hit].nan_to_num(7.0))
