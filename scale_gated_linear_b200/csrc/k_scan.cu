@@ -358,7 +358,7 @@ __device__ __forceinline__ uint32_t gate_zero(uint64_t z) {
 }
 __device__ __forceinline__ float decayed(float h, float nc, bool zero) {
   if (fabsf(h) < INFINITY) return fmaf(nc, h, h);
-  return zero ? NAN : h;
+  return zero ? NAN : h + nc;  // h, or NaN where the gate is
 }
 __device__ __forceinline__ uint64_t decayed(uint64_t h, uint64_t nc, uint32_t zero) {
   const float2 f = f2_unpack(h), c = f2_unpack(nc);

@@ -191,3 +191,24 @@ def test_infinite_values_without_output_gradients(B, L, D):
             want = oo.scan_backward(None, host(dlast), host(x), host(z), 16.0, tied, None, host(h0))[:3]
         for a, w in zip(got, want):
             same_values(a, w, F32)
+
+
+@pytest.mark.parametrize("tau", [1.0, 16.0])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("B,L,D", FORMS + [(1, 1, 2)])
+def test_nan_logits(B, L, D, dtype, tau):
+    """A NaN among the logits makes its channel NaN from its token on, an infinite state's too, and what comes before
+    it in the gradients; the step agrees."""
+    from scale_gated_linear_b200 import gated_scan_backward, gated_scan_forward, gated_scan_step
+    x, z, _, h0, dh, dlast = inputs(B, L, D, dtype, bias=1.0, state=True, seed=7)
+    z[0, L // 2, :2], h0[0, 1], dlast[0, 1] = float("nan"), float("inf"), float("-inf")
+    h, last, saved = gated_scan_forward(x.cuda(), z.cuda(), initial_state=h0.cuda(), gate_normalizer=tau)
+    got = (h, last, *gated_scan_backward(dh.cuda(), dlast.cuda(), saved))
+    with np.errstate(invalid="ignore"):
+        args = (host(x), host(z), tau, False, None, host(h0))
+        want = (*oo.scan(*args)[:2], *oo.scan_backward(host(dh), host(dlast), *args)[:3])
+    for k, (a, w) in enumerate(zip(got, want)):
+        same_values(a, w, F32 if k in (1, 4) else dtype)
+    state = h0.cuda()
+    gated_scan_step(x[:, L // 2].cuda(), z[:, L // 2].cuda(), state, gate_normalizer=tau)
+    assert torch.isnan(state[0, :2]).all() and not torch.isnan(state[1:]).any()
