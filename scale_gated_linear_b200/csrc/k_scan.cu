@@ -919,7 +919,7 @@ __global__ void __launch_bounds__(kBackRelay * 32, 2) scan_relay_backward_kernel
   constexpr uint32_t kFull = (1u << R) - 1u;
   extern __shared__ __align__(128) uint8_t dynamic[];
   __shared__ uint64_t baton[kBackRelay][32];
-  __shared__ uint32_t last_bad[32];  // lanes' channels whose last state is not finite
+  __shared__ uint64_t ends[32];  // the state after the last row
   const int w = warp_id(), lane = lane_id(), b = blockIdx.y, c0 = blockIdx.x * 64;
   const int ch = c0 + 2 * lane, n = min(max(p.D - ch, 0), 2);
   const int chunks = (p.L + R - 1) / R;
@@ -959,7 +959,7 @@ __global__ void __launch_bounds__(kBackRelay * 32, 2) scan_relay_backward_kernel
     const Raw* ds = zs + kRowsBytes / sizeof(Raw);
     uint64_t nc[R];
     const uint64_t after = row_factors<T, TAU1, TIED>(xs, zs, before, p.gate, nc);
-    if (c == chunks - 1) last_bad[lane] = not_finite(after, n);
+    if (c == chunks - 1) ends[lane] = after;
     Join join{f2_both(1.f), 0ull};
 #pragma unroll
     for (int r = R - 1; r >= 0; --r) {
@@ -980,7 +980,7 @@ __global__ void __launch_bounds__(kBackRelay * 32, 2) scan_relay_backward_kernel
       baton[to][lane] = end;
       relay_pass(to);
     } else {
-      bad = not_finite(end, n) | last_bad[lane];
+      bad = not_finite(end, n) | not_finite(ends[lane], n);
       if (p.dh0) {
         if (!bad) store_state<VEC>(p.dh0 + state_at, n, end);
         else store_some(p.dh0 + state_at, ~bad & ((1u << n) - 1u), end);
