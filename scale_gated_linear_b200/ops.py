@@ -312,11 +312,12 @@ def gated_scan(x, gate, *, mask=None, initial_state=None, gate_normalizer: float
                out=None, stream=None):
     """The gated recurrence: (h [B, L, D], last_state float32 [B, D]).
 
-    x, gate         [B, L, D]; gate holds logits: a_t = sigmoid(gate_t) ** (1 / gate_normalizer).
+    x, gate         [B, L, D], B up to 65535, L up to 2 ** 30; gate holds logits: a_t = sigmoid(gate_t) ** (1 / gate_normalizer).
                     A logit of -inf empties a finite state before its token (an infinite one: NaN).
     mask            optional valid tokens [B, L] (bool or uint8, nonzero = valid): a padded token
                     leaves the state as it is, its output is zero and its row is not read.
     initial_state   optional float32 [B, D] (default zeros); pass a call's last_state to go on.
+    gate_normalizer a number from 2 ** -10 to 2 ** 20.
     tied            the input enters as (1 - a_t) x_t instead of x_t.
     out, stream     optional tensor for h, optional stream (neither with gradients).
     """
