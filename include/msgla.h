@@ -298,7 +298,8 @@ typedef enum msgla_dtype { MSGLA_BF16 = 0, MSGLA_F16 = 1, MSGLA_F32 = 2 } msgla_
  * be views (halves of a fused projection, expanded rows with stride 0, [L, B, C]
  * memory read as [B, L, C]). An output's elements have to be distinct, and the span
  * of an output, from its first to its last element, must not meet the span of an
- * input or of another output. */
+ * input or of another output, unless both have the same strides and their rows lie side
+ * by side (dx and dz as halves of one tensor, or h beside x). */
 typedef struct msgla_rows {
   void* data;
   long long batch_stride, row_stride;

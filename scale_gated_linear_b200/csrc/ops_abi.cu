@@ -35,24 +35,44 @@ struct Device {
 
 int esize(int dtype) { return dtype == MSGLA_F32 ? 4 : 2; }
 
-// The spans of a call's buffers: an output may meet no other one.
+// The spans of a call's buffers: an output may meet no other one, unless both are rows of the same strides
+// that lie side by side (halves of one tensor).
 struct Spans {
   static constexpr int kMax = 16;
   struct One {
     const char* name;
     uintptr_t lo, hi;
     bool out;
+    long long B, L, batch, row, width;  // of rows, in bytes; width 0: no rows
   } a[kMax];
   int n = 0;
   void add(const char* name, const void* p, unsigned long long bytes, bool out) {
     if (!p || !bytes || n == kMax) return;
     const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-    a[n++] = {name, lo, lo + bytes, out};
+    a[n++] = {name, lo, lo + bytes, out, 0, 0, 0, 0, 0};
+  }
+  void add_rows(const char* name, const msgla_rows& r, long long B, long long L, long long C, int size, bool out) {
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(r.data);
+    const long long batch = r.batch_stride * size, row = r.row_stride * size, width = C * size;
+    if (n == kMax) return;
+    a[n++] = {name, lo, lo + ((B - 1) * batch + (L - 1) * row + width), out, B, L, batch, row, width};
+  }
+  // Whether a row of x and the row of y in its place lie in one slot of the inner stride, and all of those in one of
+  // the outer stride; or all inner rows of x beside all of y in a slot of the outer stride.
+  static bool side_by_side(const One& x, const One& y) {
+    if (!x.width || x.width != y.width || x.B != y.B || x.L != y.L) return false;
+    if ((x.B > 1 && x.batch != y.batch) || (x.L > 1 && x.row != y.row)) return false;
+    const long long apart = x.lo < y.lo ? static_cast<long long>(y.lo - x.lo) : static_cast<long long>(x.lo - y.lo);
+    const auto nested = [&](long long n_in, long long in, long long n_out, long long out) {
+      const long long reach = (n_in - 1) * in + x.width;  // of the inner rows of one
+      return (n_in <= 1 || apart + x.width <= in || apart >= reach) && (n_out <= 1 || apart + reach <= out);
+    };
+    return apart >= x.width && (nested(x.L, x.row, x.B, x.batch) || nested(x.B, x.batch, x.L, x.row));
   }
   int check() const {
     for (int i = 0; i < n; ++i)
       for (int j = 0; j < i; ++j)
-        if ((a[i].out || a[j].out) && a[i].lo < a[j].hi && a[j].lo < a[i].hi)
+        if ((a[i].out || a[j].out) && a[i].lo < a[j].hi && a[j].lo < a[i].hi && !side_by_side(a[i], a[j]))
           return set_error(MSGLA_ERR_INVALID_ARG, "%s and %s overlap", a[j].name, a[i].name);
     return MSGLA_OK;
   }
@@ -77,7 +97,7 @@ int take_rows(const char* name, const msgla_rows* r, long long B, long long L, l
     if (!rows_inside && !batches_inside)
       return set_error(MSGLA_ERR_INVALID_ARG, "%s: strides %lld, %lld make elements coincide", name, sb, sl);
   }
-  spans.add(name, r->data, ((B - 1) * sb + (L - 1) * sl + C) * static_cast<unsigned long long>(esize(dtype)), out);
+  spans.add_rows(name, *r, B, L, C, esize(dtype), out);
   *to = Rows{r->data, B <= 1 ? 0 : sb, L <= 1 ? 0 : sl};
   return MSGLA_OK;
 }

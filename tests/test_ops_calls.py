@@ -184,3 +184,33 @@ def test_a_captured_call_refuses_a_leaf_whose_node_is_held():
     torch.cuda.synchronize()
     assert torch.equal(y, group_norm(x, 4, w.detach())) and grads[1].shape == w.shape
     del held
+
+
+@pytest.mark.parametrize("dtype,D", [(BF16, 64), (BF16, 37), (F32, 64), (F32, 33)])
+@pytest.mark.parametrize("order", ["batch", "time"])
+def test_outputs_beside_other_rows(dtype, D, order):
+    """Rows of one tensor: h beside x and the gate, dx and dz as halves of the joint gradient, y beside its gate."""
+    B, L = 3, 70
+    joint = lambda n: (torch.zeros(B, L, n * D, dtype=dtype, device="cuda") if order == "batch" else
+                       torch.zeros(L, B, n * D, dtype=dtype, device="cuda").transpose(0, 1))
+    x, z, dh = (randn(B, L, D, dtype=dtype, seed=k) for k in range(3))
+    p = joint(3)
+    p[..., :D], p[..., D:2 * D] = x, z
+    want, last, saved = gated_scan_forward(x, z)
+    gated_scan(p[..., :D], p[..., D:2 * D], out=p[..., 2 * D:])
+    assert torch.equal(p[..., 2 * D:], want) and torch.equal(p[..., :D], x) and torch.equal(p[..., D:2 * D], z)
+    group_norm(p[..., :D], 1, gate=p[..., D:2 * D], out=p[..., 2 * D:])
+    assert torch.equal(p[..., 2 * D:], group_norm(x, 1, gate=z)) and torch.equal(p[..., D:2 * D], z)
+    state = last.clone()
+    gated_scan_step(p[:, 5, :D], p[:, 5, D:2 * D], state, out=p[:, 5, 2 * D:])
+    assert torch.equal(p[:, 5, 2 * D:], gated_scan_step(x[:, 5], z[:, 5], last.clone()))
+    g = joint(2)
+    rows = lambda t: _lib.Rows(t.data_ptr(), t.stride(0), t.stride(1))
+    cfg = _lib.ScanConfig(0, {BF16: 0, F32: 2}[dtype], D, 0, 16.0)
+    _lib.check(_lib.load().msgla_scan_backward(cfg, B, L, rows(x), rows(z), None, saved.states.data_ptr(), rows(dh), None,
+                                               rows(g[..., :D]), rows(g[..., D:]), None,
+                                               ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)))
+    dx, dz, _ = gated_scan_backward(dh, None, saved)
+    assert torch.equal(g[..., :D], dx) and torch.equal(g[..., D:], dz)
+    with pytest.raises(MSGLAError):  # shifted by less than a row's width
+        gated_scan(p[..., :D], p[..., D:2 * D], out=p[..., D + 1:2 * D + 1])
